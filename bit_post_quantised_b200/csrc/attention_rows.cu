@@ -1,0 +1,312 @@
+// attention_rows.cu -- attention of few query rows to an encoder's states:
+// one read of the keys and values, split over the keys and joined inside a
+// cluster.
+//
+//   o[r] = sum_j softmax_j(scale q[r].k[j]) v[j]   over the valid keys j.
+//
+// The G = H / Hkv query heads that share a key-value head are rows of one
+// 16-row tile (row r: query r / G, head r % G of the group), so K and V are
+// read once for all of them; with few rows the bound is that read.  A unit is
+// (batch entry, key-value head, 16 rows); a cluster of S CTAs splits its keys
+// in blocks of 16 dealt round-robin to the S * 4 warps.  A warp keeps its
+// running row maxima, sums and 16 x D output in registers, all fp32, and
+// streams its blocks with 16-byte loads straight into mma.sync fragments:
+//   - the order of the products' channels is free as long as q and k agree,
+//     so thread t of a quad takes channels 32 i + 8 t .. + 7 of a key as
+//     two k16 steps' fragments (64 consecutive bytes a quad and key);
+//   - the output channels' places in the n8 tiles are free too: row g of the
+//     quad owns channels 64 c + 8 g .. + 7 of a value row.
+// No shared memory is touched before the join, and the next block's keys are
+// in flight while this one is computed.  The probabilities go to the tensor
+// cores as the sum of two bf16 (value and remainder): the extra product is
+// free under the memory bound and leaves only the final rounding.  Masked
+// keys have their score replaced (not added to) and their value row zeroed,
+// so whatever they hold is not seen; a row without a valid key gives zeros.
+//
+// Join: the four warps of a CTA combine their (max, sum, output) through
+// shared memory, then the CTAs of the cluster through distributed shared
+// memory, each CTA writing a slice of the rows: one launch, no workspace.
+#include "internal.h"
+#include "kernel_common.cuh"
+#include "ptx.cuh"
+
+namespace tern {
+
+namespace {
+
+constexpr int kWarps = 4;
+constexpr int kRows = 16;
+
+__device__ __forceinline__ void mma_16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                          uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+__device__ __forceinline__ float exp2_fast(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+__device__ __forceinline__ uint4 load16(const uint16_t* p, bool ok) {
+  return ok ? __ldg(reinterpret_cast<const uint4*>(p)) : make_uint4(0u, 0u, 0u, 0u);
+}
+
+// hi = bf16 pair of (x, y), lo = bf16 pair of what that rounding left.
+__device__ __forceinline__ void split2(float x, float y, uint32_t& hi, uint32_t& lo) {
+  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(hi) : "f"(y), "f"(x));
+  const float rx = x - __uint_as_float(hi << 16), ry = y - __uint_as_float(hi & 0xFFFF0000u);
+  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(lo) : "f"(ry), "f"(rx));
+}
+
+__device__ __forceinline__ float2 ld_cluster_f2(uint32_t addr) {
+  float2 v;
+  asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];" : "=f"(v.x), "=f"(v.y) : "r"(addr) : "memory");
+  return v;
+}
+
+// NI: 32-channel groups of the head (D <= 32 NI); NC: 64-channel groups.
+template <int NI>
+__global__ void __launch_bounds__(kWarps * 32, 2) attention_rows_kernel(const __grid_constant__ AttnArgs a, int splits) {
+  constexpr int NC = (NI + 1) / 2;
+  constexpr int DP = 64 * NC;
+  __shared__ float sm_ml[kWarps][kRows][2];      // running maximum (log2 units) and sum of each warp
+  __shared__ __align__(16) float sm_o[kWarps][kRows][DP];
+  __shared__ float cta_ml[kRows][2];             // the CTA's own, read by the cluster
+  __shared__ __align__(16) float cta_o[kRows][DP];
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int g = lane >> 2, t = lane & 3;
+  const int split = int(blockIdx.x) % splits;
+  const long long unit = blockIdx.x / splits;
+  const int G = a.H / a.Hkv;
+  const long long R = (long long)a.Lq * G;
+  const int row_blocks = int((R + kRows - 1) / kRows);
+  const int rb = int(unit % row_blocks);
+  const int hk = int(unit / row_blocks % a.Hkv);
+  const int b = int(unit / row_blocks / a.Hkv);
+  pdl_wait();
+  pdl_trigger();
+  const int len = a.kv_len ? max(0, min(a.Lk, a.kv_len[b])) : a.Lk;
+  const uint8_t* mask = a.key_mask ? a.key_mask + b * a.mask_ld : nullptr;
+  const uint16_t* kp = a.k + b * a.k_b + hk * a.k_h;
+  const uint16_t* vp = a.v + b * a.v_b + hk * a.v_h;
+
+  // The query rows' fragments.
+  uint32_t q[2 * NI][4];
+#pragma unroll
+  for (int half = 0; half < 2; ++half) {
+    const long long r = (long long)rb * kRows + g + 8 * half;
+    const uint16_t* qp = a.q + b * a.q_b + (r / G) * a.q_l + (hk * G + r % G) * a.q_h;
+#pragma unroll
+    for (int i = 0; i < NI; ++i) {
+      const int d = 32 * i + 8 * t;
+      const uint4 v = load16(qp + d, r < R && d < a.D);
+      q[2 * i][half] = v.x, q[2 * i][2 + half] = v.y;
+      q[2 * i + 1][half] = v.z, q[2 * i + 1][2 + half] = v.w;
+    }
+  }
+  float m[2] = {-INFINITY, -INFINITY}, sum[2] = {0.f, 0.f};
+  float o[8 * NC][4];
+#pragma unroll
+  for (int j = 0; j < 8 * NC; ++j) o[j][0] = o[j][1] = o[j][2] = o[j][3] = 0.f;
+
+  const int blocks = (len + 15) / 16;
+  const int stride = splits * kWarps;
+  uint4 kv[2][NI];
+  auto load_k = [&](int blk) {
+#pragma unroll
+    for (int nt = 0; nt < 2; ++nt) {
+      const int key = blk * 16 + nt * 8 + g;
+#pragma unroll
+      for (int i = 0; i < NI; ++i) {
+        const int d = 32 * i + 8 * t;
+        kv[nt][i] = load16(kp + (long long)key * a.k_l + d, key < len && d < a.D);
+      }
+    }
+  };
+  int blk = split * kWarps + warp;
+  if (blk < blocks) load_k(blk);
+  for (; blk < blocks; blk += stride) {
+    // Keys of this thread: its score columns and its value rows are the same.
+    bool ok[4];
+    uint4 vv[4][NC];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const int key = blk * 16 + 2 * t + (e & 1) + (e >> 1) * 8;
+      ok[e] = key < len && (!mask || mask[key]);
+#pragma unroll
+      for (int c = 0; c < NC; ++c) {
+        const int d = 64 * c + 8 * g;
+        vv[e][c] = load16(vp + (long long)key * a.v_l + d, ok[e] && d < a.D);
+      }
+    }
+    float s[2][4];
+#pragma unroll
+    for (int nt = 0; nt < 2; ++nt) {
+      s[nt][0] = s[nt][1] = s[nt][2] = s[nt][3] = 0.f;
+#pragma unroll
+      for (int i = 0; i < NI; ++i) {
+        mma_16816(s[nt], q[2 * i][0], q[2 * i][1], q[2 * i][2], q[2 * i][3], kv[nt][i].x, kv[nt][i].y);
+        mma_16816(s[nt], q[2 * i + 1][0], q[2 * i + 1][1], q[2 * i + 1][2], q[2 * i + 1][3], kv[nt][i].z, kv[nt][i].w);
+      }
+    }
+    if (blk + stride < blocks) load_k(blk + stride);
+    float top[2];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+#pragma unroll
+      for (int nt = 0; nt < 2; ++nt)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          float& v = s[nt][2 * h + e];
+          v = ok[2 * nt + e] ? v * a.scale_log2 : -INFINITY;
+        }
+      top[h] = fmaxf(fmaxf(s[0][2 * h], s[0][2 * h + 1]), fmaxf(s[1][2 * h], s[1][2 * h + 1]));
+      top[h] = fmaxf(top[h], __shfl_xor_sync(0xffffffffu, top[h], 1));
+      top[h] = fmaxf(top[h], __shfl_xor_sync(0xffffffffu, top[h], 2));
+    }
+    if (__any_sync(0xffffffffu, top[0] > m[0] || top[1] > m[1])) {
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const float to = fmaxf(m[h], top[h]);
+        const float f = to == -INFINITY ? 1.f : exp2_fast(m[h] - to);
+        m[h] = to;
+        sum[h] *= f;
+#pragma unroll
+        for (int j = 0; j < 8 * NC; ++j) o[j][2 * h] *= f, o[j][2 * h + 1] *= f;
+      }
+    }
+    uint32_t hi[4], lo[4];  // A fragment of P: (row g | g + 8) x (keys 2t, 2t + 1 | + 8)
+#pragma unroll
+    for (int nt = 0; nt < 2; ++nt)
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const float base = m[h] == -INFINITY ? 0.f : m[h];
+        const float p0 = exp2_fast(s[nt][2 * h] - base), p1 = exp2_fast(s[nt][2 * h + 1] - base);
+        sum[h] += p0 + p1;
+        split2(p0, p1, hi[2 * nt + h], lo[2 * nt + h]);
+      }
+#pragma unroll
+    for (int c = 0; c < NC; ++c) {
+      const uint32_t* w0 = &vv[0][c].x;
+      const uint32_t* w1 = &vv[1][c].x;
+      const uint32_t* w2 = &vv[2][c].x;
+      const uint32_t* w3 = &vv[3][c].x;
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const uint32_t sel = e ? 0x7632u : 0x5410u;
+          const uint32_t b0 = __byte_perm(w0[i], w1[i], sel), b1 = __byte_perm(w2[i], w3[i], sel);
+          float(&d)[4] = o[8 * c + 2 * i + e];
+          mma_16816(d, hi[0], hi[1], hi[2], hi[3], b0, b1);
+          mma_16816(d, lo[0], lo[1], lo[2], lo[3], b0, b1);
+        }
+    }
+  }
+  // ---- join
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    sum[h] += __shfl_xor_sync(0xffffffffu, sum[h], 1);
+    sum[h] += __shfl_xor_sync(0xffffffffu, sum[h], 2);
+    if (t == 0) {
+      sm_ml[warp][g + 8 * h][0] = m[h];
+      sm_ml[warp][g + 8 * h][1] = sum[h];
+    }
+#pragma unroll
+    for (int c = 0; c < NC; ++c)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {  // channels 64 c + 8 (2t + e) + 0..7
+        float4* dst = reinterpret_cast<float4*>(&sm_o[warp][g + 8 * h][64 * c + 16 * t + 8 * e]);
+        dst[0] = make_float4(o[8 * c + 0][2 * h + e], o[8 * c + 1][2 * h + e], o[8 * c + 2][2 * h + e], o[8 * c + 3][2 * h + e]);
+        dst[1] = make_float4(o[8 * c + 4][2 * h + e], o[8 * c + 5][2 * h + e], o[8 * c + 6][2 * h + e], o[8 * c + 7][2 * h + e]);
+      }
+  }
+  __syncthreads();
+  // The CTA's own (max, sum, output): thread = (row, part of the channels).
+  {
+    const int r = threadIdx.x >> 3, part = threadIdx.x & 7;
+    float top = -INFINITY;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) top = fmaxf(top, sm_ml[w][r][0]);
+    float f[kWarps], total = 0.f;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) {
+      const float mw = sm_ml[w][r][0];
+      f[w] = mw == -INFINITY ? 0.f : exp2_fast(mw - top);
+      // A row whose scores are NaN has no maximum; its sum is NaN and stays so.
+      total += sm_ml[w][r][1] * (mw == -INFINITY ? 1.f : f[w]);
+    }
+    if (part == 0) cta_ml[r][0] = top, cta_ml[r][1] = total;
+    for (int d = part * 2; d < DP; d += 16) {
+      float x = 0.f, y = 0.f;
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) {
+        const float2 v = *reinterpret_cast<const float2*>(&sm_o[w][r][d]);
+        x = fmaf(v.x, f[w], x);
+        y = fmaf(v.y, f[w], y);
+      }
+      *reinterpret_cast<float2*>(&cta_o[r][d]) = make_float2(x, y);
+    }
+  }
+  if (splits > 1) cluster_sync();
+  else __syncthreads();
+  const uint32_t ml0 = smem_u32(&cta_ml[0][0]), o0 = smem_u32(&cta_o[0][0]);
+  for (int i = split * (kWarps * 32) + int(threadIdx.x); i < kRows * DP / 2; i += splits * (kWarps * 32)) {
+    const int r = i / (DP / 2), d = 2 * (i % (DP / 2));
+    const long long row = (long long)rb * kRows + r;
+    if (row >= R || d >= a.D) continue;
+    float x = 0.f, y = 0.f, total = 0.f, top = -INFINITY;
+    if (splits == 1) {
+      total = cta_ml[r][1];
+      x = cta_o[r][d], y = cta_o[r][d + 1];
+    } else {
+      for (int s = 0; s < splits; ++s) top = fmaxf(top, ld_cluster_f2(mapa_shared(ml0 + r * 8, s)).x);
+      for (int s = 0; s < splits; ++s) {
+        const float2 ml = ld_cluster_f2(mapa_shared(ml0 + r * 8, s));
+        const float2 v = ld_cluster_f2(mapa_shared(o0 + (r * DP + d) * 4, s));
+        const float f = ml.x == -INFINITY ? 0.f : exp2_fast(ml.x - top);
+        total += ml.y * (ml.x == -INFINITY ? 1.f : f);
+        x = fmaf(v.x, f, x);
+        y = fmaf(v.y, f, y);
+      }
+    }
+    const float inv = total == 0.f ? 0.f : 1.f / total;
+    uint32_t w;
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(w) : "f"(y * inv), "f"(x * inv));
+    *reinterpret_cast<uint32_t*>(a.o + b * a.o_b + (row / G) * a.o_l + (hk * G + row % G) * a.o_h + d) = w;
+  }
+  // No CTA leaves while another may still read its shared memory.
+  if (splits > 1) cluster_sync_relaxed();
+}
+
+template <int NI>
+cudaError_t launch_ni(const AttnArgs& a, int splits, cudaStream_t stream) {
+  const long long rows = (long long)a.Lq * (a.H / a.Hkv);
+  const long long units = (rows + kRows - 1) / kRows * a.Hkv * a.B;
+  return launch_pdl(attention_rows_kernel<NI>, dim3(unsigned(units * splits)), dim3(kWarps * 32), 0, stream, unsigned(splits),
+                    a, splits);
+}
+
+}  // namespace
+
+cudaError_t launch_attention_rows(const AttnArgs& a, int sms, cudaStream_t stream) {
+  const long long rows = (long long)a.Lq * (a.H / a.Hkv);
+  const long long units = (rows + kRows - 1) / kRows * a.Hkv * a.B;
+  // Split the keys while CTAs are fewer than two per SM and each warp keeps a block of 16 keys.
+  int splits = 1;
+  while (splits < 8 && units * splits < 2 * sms && splits * 2 * kWarps <= (a.Lk + 15) / 16) splits *= 2;
+  switch ((a.D + 31) / 32) {
+    case 1: return launch_ni<1>(a, splits, stream);
+    case 2: return launch_ni<2>(a, splits, stream);
+    case 3: return launch_ni<3>(a, splits, stream);
+    case 4: return launch_ni<4>(a, splits, stream);
+  }
+  return cudaErrorInvalidValue;
+}
+
+}  // namespace tern

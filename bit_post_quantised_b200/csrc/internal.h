@@ -146,5 +146,61 @@ cudaError_t launch_quantize_act_e4m3(const __nv_bfloat16* x, int M, int K, uint8
                                      cudaStream_t stream);
 cudaError_t launch_ternary_fp8(const Batch& batch, int pairs, cudaStream_t stream);
 
+// Rotary table: the frequency and axis of every channel pair.
+constexpr int kRopeMaxPairs = 128;
+struct RopeFreqs {
+  double omega[kRopeMaxPairs];  // theta^(-2 i / d_a)
+  uint8_t axis[kRopeMaxPairs];
+  int pairs, n_axes;
+};
+// cs [L][pairs][2] from ids [L][n_axes].
+cudaError_t launch_rope_table(const float* ids, long long L, const RopeFreqs& f, float* cs, cudaStream_t stream);
+
+// Rotation of up to kRopeTensors head tensors of the same tokens.
+constexpr int kRopeTensors = 4;
+struct RopeTensor {
+  const uint16_t* x;
+  uint16_t* y;
+  long long x_b, x_l, x_h, y_b, y_l, y_h;  // elements between batch entries, tokens, heads
+  int heads;
+};
+struct RopeArgs {
+  RopeTensor t[kRopeTensors];  // unused ones have no heads
+  const float* cs;
+  long long rows, L;  // rows = batch * L
+  int heads;          // of all tensors
+  int head_dim, rot;
+  int cs_per_batch;   // the table has a row per (batch entry, token), not per token
+  int units, turned_units, heads_par, rows_par;  // set by launch_rope
+};
+cudaError_t launch_rope(RopeArgs a, bool halves, cudaStream_t stream);
+
+// Gated residual update with the norms around it; rows of K elements, K % 8 == 0.
+constexpr int kNormNone = 0, kNormRms = 1, kNormLayer = 2;
+constexpr int kResNormMaxK = 16384;
+struct ResNormArgs {
+  const uint16_t *x, *o;
+  uint16_t *x_out, *h;  // h may be null
+  const uint16_t *gate, *scale, *shift, *post_weight, *pre_weight;  // each may be null (scale and shift together)
+  long long M, ld_x, ld_o, ld_xo, ld_h, mod_ld, tokens_per_row;
+  int K, post, pre, gate_tanh;
+  float post_eps, pre_eps, residual_scale;
+};
+cudaError_t launch_gated_residual_norm(const ResNormArgs& a, cudaStream_t stream);
+
+// Attention of q [B, Lq, H, D] to k, v [B, Lk, Hkv, D] (strides in elements).
+constexpr int kAttnMaxD = 128;
+struct AttnArgs {
+  const uint16_t *q, *k, *v;
+  uint16_t* o;
+  long long q_b, q_l, q_h, k_b, k_l, k_h, v_b, v_l, v_h, o_b, o_l, o_h;
+  const int* kv_len;        // [B] or null
+  const uint8_t* key_mask;  // [B] rows mask_ld apart, or null
+  long long mask_ld;
+  int B, Lq, Lk, H, Hkv, D;
+  float scale_log2;         // softmax scale * log2(e)
+};
+// One read of k and v for up to 16 packed query rows; see attention_rows.cu.
+cudaError_t launch_attention_rows(const AttnArgs& a, int sms, cudaStream_t stream);
 
 }  // namespace tern

@@ -910,6 +910,286 @@ tern_status tern_linear_e4m3(const void* xq, const float* a, int64_t M, int64_t 
   return TERN_OK;
 }
 
+// ------------------------------------------------- operators between linears
+namespace {
+
+constexpr int64_t kMaxStride = int64_t(1) << 38;
+
+// A [B, L, heads, D] bf16 tensor: strides in elements, adjacent channels.
+struct Heads {
+  const void* p;
+  int64_t B, L, H, D, b, l, h;
+  bool empty() const { return !p || B <= 0 || L <= 0 || H <= 0; }
+  int64_t span() const { return (B - 1) * b + (L - 1) * l + (H - 1) * h + D; }
+};
+
+// 16-byte accesses: every stride that is used a multiple of 8; a stride of 0
+// (a broadcast) only where `read`.
+bool strides_ok(const Heads& t, bool read) {
+  const int64_t n[3] = {t.B, t.L, t.H}, s[3] = {t.b, t.l, t.h};
+  for (int i = 0; i < 3; ++i)
+    if (n[i] > 1 && (s[i] % 8 != 0 || s[i] < (read ? 0 : 8) || s[i] > kMaxStride)) return false;
+  return true;
+}
+
+// The elements of a written tensor are distinct where each dimension's stride
+// covers the extent of the dimensions with smaller strides.
+bool elements_distinct(const Heads& t) {
+  std::pair<int64_t, int64_t> d[3] = {{t.b, t.B}, {t.l, t.L}, {t.h, t.H}};
+  std::sort(d, d + 3);
+  int64_t extent = t.D;
+  for (const auto& [stride, n] : d) {
+    if (n <= 1) continue;
+    if (stride < extent) return false;
+    extent += (n - 1) * stride;
+  }
+  return true;
+}
+
+// Whether two head tensors share a byte: by their spans, or exactly (as
+// regions of rows) where both are column slices of rows equally far apart.
+bool heads_overlap(const Heads& a, const Heads& b) {
+  if (a.empty() || b.empty()) return false;
+  if (!overlaps(a.p, size_t(a.span()) * 2, b.p, size_t(b.span()) * 2)) return false;
+  auto rows = [](const Heads& t, int64_t* n, int64_t* width) {
+    *width = (t.H - 1) * t.h + t.D;
+    if (t.l < *width || (t.B > 1 && t.b % t.l != 0)) return false;
+    *n = (t.B - 1) * (t.B > 1 ? t.b / t.l : 0) + t.L;
+    return true;
+  };
+  int64_t na, wa, nb, wb;
+  if (a.l <= 0 || a.l != b.l || !rows(a, &na, &wa) || !rows(b, &nb, &wb)) return true;
+  return regions_overlap(a.p, na, size_t(wa) * 2, size_t(a.l) * 2, b.p, nb, size_t(wb) * 2, size_t(b.l) * 2);
+}
+
+bool overlaps_flat(const Heads& t, const void* p, size_t bytes) {
+  return !t.empty() && overlaps(t.p, size_t(t.span()) * 2, p, bytes);
+}
+
+const uint16_t* u16(const void* p) { return static_cast<const uint16_t*>(p); }
+uint16_t* u16w(void* p) { return static_cast<uint16_t*>(p); }
+
+}  // namespace
+
+tern_status tern_rope_table(const float* ids, int64_t L, int n_axes, const int* axis_dims, double theta, float* cs,
+                            tern_stream_t stream) {
+  if (L < 0) return fail(TERN_ERR_INVALID_ARG, "negative L=%lld", (long long)L);
+  if (n_axes < 1 || n_axes > 4) return fail(TERN_ERR_UNSUPPORTED_SHAPE, "rope_table: 1 to 4 axes, got %d", n_axes);
+  if (!axis_dims) return fail(TERN_ERR_INVALID_ARG, "null axis_dims");
+  if (!(theta > 0) || !std::isfinite(theta)) return fail(TERN_ERR_INVALID_ARG, "theta must be finite and > 0");
+  if (L > INT32_MAX) return fail(TERN_ERR_UNSUPPORTED_SHAPE, "rope_table: L above 2^31 - 1");
+  RopeFreqs f{};
+  f.n_axes = n_axes;
+  for (int a = 0; a < n_axes; ++a) {
+    const int d = axis_dims[a];
+    if (d < 2 || d % 2 != 0 || f.pairs + d / 2 > kRopeMaxPairs || d > 2 * kRopeMaxPairs)
+      return fail(TERN_ERR_UNSUPPORTED_SHAPE, "rope_table: axis sizes are even, >= 2 and at most %d in all (axis %d has %d)",
+                  2 * kRopeMaxPairs, a, d);
+    for (int i = 0; i < d / 2; ++i) {
+      f.omega[f.pairs] = std::pow(theta, -2.0 * i / d);
+      f.axis[f.pairs++] = uint8_t(a);
+    }
+  }
+  if (L == 0) return TERN_OK;
+  if (!ids || !cs) return fail(TERN_ERR_INVALID_ARG, "null ids or cs");
+  if (!aligned(ids, 4) || !aligned(cs, 8))
+    return fail(TERN_ERR_MISALIGNED, "ids needs 4-byte, cs 8-byte alignment");
+  if (overlaps(cs, size_t(L) * f.pairs * 8, ids, size_t(L) * n_axes * 4))
+    return fail(TERN_ERR_INVALID_ARG, "cs overlaps ids");
+  int dev;
+  DeviceState* ds;
+  tern_status s;
+  if ((s = current_device(&dev, &ds)) != TERN_OK) return s;
+  cudaError_t e = launch_rope_table(ids, L, f, cs, reinterpret_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(e, "rope_table launch");
+  return TERN_OK;
+}
+
+tern_status tern_rope(const tern_rope_tensor* tensors, int count, int64_t B, int64_t L, int64_t head_dim,
+                      const float* cs, int64_t cs_rows, int64_t P, int layout, tern_stream_t stream) {
+  if (count < 0 || (count > 0 && !tensors)) return fail(TERN_ERR_INVALID_ARG, "bad count or null tensors");
+  if (count > kRopeTensors) return fail(TERN_ERR_UNSUPPORTED_SHAPE, "rope: at most %d tensors", kRopeTensors);
+  if (layout != TERN_ROPE_PAIRS && layout != TERN_ROPE_HALVES) return fail(TERN_ERR_INVALID_ARG, "unknown layout %d", layout);
+  if (B < 0 || L < 0) return fail(TERN_ERR_INVALID_ARG, "negative size B=%lld L=%lld", (long long)B, (long long)L);
+  if (head_dim < 8 || head_dim % 8 != 0 || head_dim > 2 * kRopeMaxPairs || P < 8 || P % 8 != 0 || 2 * P > head_dim)
+    return fail(TERN_ERR_UNSUPPORTED_SHAPE, "rope: need head_dim %% 8 == 0, 2P %% 16 == 0, 2P <= head_dim <= %d (head_dim=%lld P=%lld)",
+                2 * kRopeMaxPairs, (long long)head_dim, (long long)P);
+  if (B > INT32_MAX || L > INT32_MAX || (B && L > INT32_MAX / B))
+    return fail(TERN_ERR_UNSUPPORTED_SHAPE, "rope: B * L above 2^31 - 1");
+  RopeArgs a{};
+  Heads x[kRopeTensors], y[kRopeTensors];
+  for (int i = 0; i < count; ++i) {
+    const tern_rope_tensor& t = tensors[i];
+    if (t.heads < 0) return fail(TERN_ERR_INVALID_ARG, "tensor %d: negative heads", i);
+    if (t.heads > (1 << 20)) return fail(TERN_ERR_UNSUPPORTED_SHAPE, "tensor %d: heads above 2^20", i);
+    x[i] = Heads{t.x, B, L, t.heads, head_dim, t.x_b, t.x_l, t.x_h};
+    y[i] = Heads{t.y, B, L, t.heads, head_dim, t.y_b, t.y_l, t.y_h};
+    a.t[i] = RopeTensor{u16(t.x), u16w(t.y), t.x_b, t.x_l, t.x_h, t.y_b, t.y_l, t.y_h, int(t.heads)};
+    a.heads += int(t.heads);
+  }
+  if (B == 0 || L == 0 || a.heads == 0) return TERN_OK;
+  if (!cs) return fail(TERN_ERR_INVALID_ARG, "null cs");
+  if (!aligned(cs, 16)) return fail(TERN_ERR_MISALIGNED, "cs needs 16-byte alignment");
+  if (cs_rows != L && cs_rows != B * L)
+    return fail(TERN_ERR_INVALID_ARG, "rope: cs has %lld rows; L=%lld or B * L=%lld wanted", (long long)cs_rows, (long long)L,
+                (long long)(B * L));
+  for (int i = 0; i < count; ++i) {
+    if (tensors[i].heads == 0) continue;
+    if (!x[i].p || !y[i].p) return fail(TERN_ERR_INVALID_ARG, "tensor %d: null x or y", i);
+    if (!aligned(x[i].p, 16) || !aligned(y[i].p, 16))
+      return fail(TERN_ERR_MISALIGNED, "tensor %d: x and y need 16-byte alignment", i);
+    if (!strides_ok(x[i], true) || !strides_ok(y[i], false) || !elements_distinct(y[i]))
+      return fail(TERN_ERR_INVALID_ARG, "tensor %d: strides must be multiples of 8, >= 0 in x, and keep the elements of y apart", i);
+  }
+  for (int i = 0; i < count; ++i) {
+    if (overlaps_flat(y[i], cs, size_t(cs_rows) * size_t(P) * 8))
+      return fail(TERN_ERR_INVALID_ARG, "tensor %d: y overlaps the table", i);
+    for (int j = 0; j < count; ++j) {
+      const bool in_place = i == j && x[i].p == y[i].p && (B <= 1 || x[i].b == y[i].b) && (L <= 1 || x[i].l == y[i].l) &&
+                            (x[i].H <= 1 || x[i].h == y[i].h);
+      if ((!in_place && heads_overlap(y[i], x[j])) || (i != j && heads_overlap(y[i], y[j])))
+        return fail(TERN_ERR_INVALID_ARG, "y of tensor %d overlaps tensor %d", i, j);
+    }
+  }
+  a.cs = cs;
+  a.rows = B * L;
+  a.L = L;
+  a.head_dim = int(head_dim);
+  a.rot = int(2 * P);
+  a.cs_per_batch = cs_rows != L;
+  int dev;
+  DeviceState* ds;
+  tern_status s;
+  if ((s = current_device(&dev, &ds)) != TERN_OK) return s;
+  cudaError_t e = launch_rope(a, layout == TERN_ROPE_HALVES, reinterpret_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(e, "rope launch");
+  return TERN_OK;
+}
+
+tern_status tern_attention(const tern_attention_args* args, tern_stream_t stream) {
+  if (!args) return fail(TERN_ERR_INVALID_ARG, "null args");
+  const tern_attention_args& t = *args;
+  if (t.B < 0 || t.Lq < 0 || t.Lk < 0 || t.H < 0 || t.Hkv < 0 || t.D < 0)
+    return fail(TERN_ERR_INVALID_ARG, "negative size B=%lld Lq=%lld Lk=%lld H=%lld Hkv=%lld D=%lld", (long long)t.B,
+                (long long)t.Lq, (long long)t.Lk, (long long)t.H, (long long)t.Hkv, (long long)t.D);
+  if (t.D < 8 || t.D % 8 != 0 || t.D > kAttnMaxD)
+    return fail(TERN_ERR_UNSUPPORTED_SHAPE, "attention: need D %% 8 == 0 and 8 <= D <= %d, got %lld", kAttnMaxD, (long long)t.D);
+  if (t.B == 0 || t.Lq == 0 || t.H == 0) return TERN_OK;
+  const int64_t kMaxL = int64_t(1) << 30, kMaxBH = int64_t(1) << 20;
+  if (t.Hkv == 0 || t.H % t.Hkv != 0)
+    return fail(TERN_ERR_UNSUPPORTED_SHAPE, "attention: H must be a multiple of Hkv (H=%lld Hkv=%lld)", (long long)t.H,
+                (long long)t.Hkv);
+  if (t.Lq >= kMaxL || t.Lk >= kMaxL || t.B >= kMaxBH || t.H >= kMaxBH || t.B * t.H >= kMaxBH)
+    return fail(TERN_ERR_UNSUPPORTED_SHAPE, "attention: Lq and Lk are below 2^30, B * H below 2^20");
+  if (!(t.scale > 0.f) || !std::isfinite(t.scale)) return fail(TERN_ERR_INVALID_ARG, "scale must be finite and > 0");
+  if (!t.q || !t.o || (t.Lk > 0 && (!t.k || !t.v))) return fail(TERN_ERR_INVALID_ARG, "null q, k, v or o");
+  if (!aligned(t.q, 16) || !aligned(t.o, 16) || (t.Lk > 0 && (!aligned(t.k, 16) || !aligned(t.v, 16))))
+    return fail(TERN_ERR_MISALIGNED, "q, k, v and o need 16-byte alignment");
+  if (!aligned(t.kv_len, 4)) return fail(TERN_ERR_MISALIGNED, "kv_len needs 4-byte alignment");
+  if (t.key_mask && t.B > 1 && (t.mask_ld < 0 || t.mask_ld > kMaxStride))
+    return fail(TERN_ERR_INVALID_ARG, "mask_ld=%lld", (long long)t.mask_ld);
+  const Heads q{t.q, t.B, t.Lq, t.H, t.D, t.q_b, t.q_l, t.q_h}, o{t.o, t.B, t.Lq, t.H, t.D, t.o_b, t.o_l, t.o_h};
+  const Heads k{t.k, t.B, t.Lk, t.Hkv, t.D, t.k_b, t.k_l, t.k_h}, v{t.v, t.B, t.Lk, t.Hkv, t.D, t.v_b, t.v_l, t.v_h};
+  if (!strides_ok(q, true) || !strides_ok(k, true) || !strides_ok(v, true) || !strides_ok(o, false) || !elements_distinct(o))
+    return fail(TERN_ERR_INVALID_ARG, "attention: strides must be multiples of 8, >= 0, and keep the elements of o apart");
+  if (heads_overlap(o, q) || heads_overlap(o, k) || heads_overlap(o, v) ||
+      overlaps_flat(o, t.kv_len, t.kv_len ? size_t(t.B) * 4 : 0) ||
+      overlaps_flat(o, t.key_mask, t.key_mask ? size_t((t.B - 1) * (t.B > 1 ? t.mask_ld : 0) + t.Lk) : 0))
+    return fail(TERN_ERR_INVALID_ARG, "o overlaps an input");
+  AttnArgs a{};
+  a.q = u16(t.q), a.k = u16(t.k), a.v = u16(t.v), a.o = u16w(t.o);
+  a.q_b = t.q_b, a.q_l = t.q_l, a.q_h = t.q_h;
+  a.k_b = t.k_b, a.k_l = t.k_l, a.k_h = t.k_h;
+  a.v_b = t.v_b, a.v_l = t.v_l, a.v_h = t.v_h;
+  a.o_b = t.o_b, a.o_l = t.o_l, a.o_h = t.o_h;
+  a.kv_len = t.kv_len;
+  a.key_mask = t.key_mask;
+  a.mask_ld = t.mask_ld;
+  a.B = int(t.B), a.Lq = int(t.Lq), a.Lk = int(t.Lk), a.H = int(t.H), a.Hkv = int(t.Hkv), a.D = int(t.D);
+  a.scale_log2 = t.scale * 1.44269504088896340736f;
+  if ((t.Lq * (t.H / t.Hkv) + 15) / 16 * t.Hkv * t.B * 8 > INT32_MAX)
+    return fail(TERN_ERR_UNSUPPORTED_SHAPE, "attention: too many query rows");
+  int dev;
+  DeviceState* ds;
+  tern_status s;
+  if ((s = current_device(&dev, &ds)) != TERN_OK) return s;
+  cudaError_t e = launch_attention_rows(a, ds->sms, reinterpret_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(e, "attention launch");
+  return TERN_OK;
+}
+
+static_assert(kNormNone == TERN_NORM_NONE && kNormRms == TERN_NORM_RMS && kNormLayer == TERN_NORM_LAYER,
+              "kernel and ABI norm codes");
+
+tern_status tern_gated_residual_norm(const tern_gated_residual_norm_args* args, tern_stream_t stream) {
+  if (!args) return fail(TERN_ERR_INVALID_ARG, "null args");
+  const tern_gated_residual_norm_args& t = *args;
+  if (t.M < 0) return fail(TERN_ERR_INVALID_ARG, "negative M=%lld", (long long)t.M);
+  if (t.K < 8 || t.K % 8 != 0 || t.K > kResNormMaxK || t.M > INT32_MAX || t.tokens_per_row < 1)
+    return fail(TERN_ERR_UNSUPPORTED_SHAPE, "gated_residual_norm: need K %% 8 == 0, 8 <= K <= %d, M < 2^31, tokens_per_row >= 1 "
+                "(M=%lld K=%lld tokens_per_row=%lld)", kResNormMaxK, (long long)t.M, (long long)t.K, (long long)t.tokens_per_row);
+  for (const auto& [kind, eps] : {std::pair<int, float>{t.post_norm, t.post_eps}, {t.pre_norm, t.pre_eps}}) {
+    if (kind != TERN_NORM_NONE && kind != TERN_NORM_RMS && kind != TERN_NORM_LAYER)
+      return fail(TERN_ERR_INVALID_ARG, "unknown norm %d", kind);
+    if (kind != TERN_NORM_NONE && (!(eps >= 0.f) || !std::isfinite(eps)))
+      return fail(TERN_ERR_INVALID_ARG, "eps must be finite and >= 0");
+  }
+  if (!std::isfinite(t.residual_scale)) return fail(TERN_ERR_INVALID_ARG, "residual_scale must be finite");
+  if (t.M == 0) return TERN_OK;  // tensors without rows may have no address
+  if (!t.scale != !t.shift) return fail(TERN_ERR_INVALID_ARG, "scale and shift are given together");
+  if ((t.post_weight && t.post_norm == TERN_NORM_NONE) || (t.pre_weight && t.pre_norm == TERN_NORM_NONE))
+    return fail(TERN_ERR_INVALID_ARG, "a weight without its norm");
+  if (!t.h && (t.pre_norm != TERN_NORM_NONE || t.scale))
+    return fail(TERN_ERR_INVALID_ARG, "a norm or modulation of the updated stream without h");
+  if (t.gate_tanh && !t.gate) return fail(TERN_ERR_INVALID_ARG, "gate_tanh without a gate");
+  if (!t.x || !t.o || !t.x_out) return fail(TERN_ERR_INVALID_ARG, "null x, o or x_out");
+  if (!aligned(t.x, 16) || !aligned(t.o, 16) || !aligned(t.x_out, 16) || !aligned(t.h, 16) || !aligned(t.gate, 16) ||
+      !aligned(t.scale, 16) || !aligned(t.shift, 16) || !aligned(t.post_weight, 16) || !aligned(t.pre_weight, 16))
+    return fail(TERN_ERR_MISALIGNED, "every tensor needs 16-byte alignment");
+  auto row_stride = [&](int64_t ld) { return ld >= t.K && ld % 8 == 0 && ld <= kMaxStride; };
+  if (!row_stride(t.ld_x) || !row_stride(t.ld_o) || !row_stride(t.ld_x_out) || (t.h && !row_stride(t.ld_h)))
+    return fail(TERN_ERR_INVALID_ARG, "row strides need >= K=%lld and multiples of 8", (long long)t.K);
+  const bool mod = t.gate || t.scale;
+  if (mod && !row_stride(t.mod_ld)) return fail(TERN_ERR_INVALID_ARG, "mod_ld needs >= K=%lld and a multiple of 8", (long long)t.K);
+  const size_t w = size_t(t.K) * 2;
+  const int64_t G = (t.M + t.tokens_per_row - 1) / t.tokens_per_row;
+  struct In {
+    const void* p;
+    int64_t rows, ld;
+    bool alias;  // may be an output itself
+  };
+  const In ins[] = {{t.x, t.M, t.ld_x, true},        {t.o, t.M, t.ld_o, true},
+                    {t.gate, G, t.mod_ld, false},    {t.scale, G, t.mod_ld, false},
+                    {t.shift, G, t.mod_ld, false},   {t.post_weight, 1, t.K, false},
+                    {t.pre_weight, 1, t.K, false}};
+  const In outs[] = {{t.x_out, t.M, t.ld_x_out, false}, {t.h, t.M, t.ld_h, false}};
+  for (const In& y : outs) {
+    if (!y.p) continue;
+    for (const In& x : ins) {
+      if (!x.p || (x.alias && x.p == y.p && x.ld == y.ld)) continue;
+      if (regions_overlap(y.p, y.rows, w, size_t(y.ld) * 2, x.p, x.rows, w, size_t(x.ld) * 2))
+        return fail(TERN_ERR_INVALID_ARG, "an output overlaps an input without being it");
+    }
+  }
+  if (t.h && regions_overlap(t.x_out, t.M, w, size_t(t.ld_x_out) * 2, t.h, t.M, w, size_t(t.ld_h) * 2))
+    return fail(TERN_ERR_INVALID_ARG, "x_out and h overlap");
+  ResNormArgs a{};
+  a.x = u16(t.x), a.o = u16(t.o), a.x_out = u16w(t.x_out), a.h = u16w(t.h);
+  a.gate = u16(t.gate), a.scale = u16(t.scale), a.shift = u16(t.shift);
+  a.post_weight = u16(t.post_weight), a.pre_weight = u16(t.pre_weight);
+  a.M = t.M, a.ld_x = t.ld_x, a.ld_o = t.ld_o, a.ld_xo = t.ld_x_out, a.ld_h = t.ld_h, a.mod_ld = mod ? t.mod_ld : 0;
+  a.tokens_per_row = t.tokens_per_row;
+  a.K = int(t.K), a.post = t.post_norm, a.pre = t.pre_norm, a.gate_tanh = t.gate_tanh != 0;
+  a.post_eps = t.post_eps, a.pre_eps = t.pre_eps, a.residual_scale = t.residual_scale;
+  int dev;
+  DeviceState* ds;
+  tern_status s;
+  if ((s = current_device(&dev, &ds)) != TERN_OK) return s;
+  cudaError_t e = launch_gated_residual_norm(a, reinterpret_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(e, "gated_residual_norm launch");
+  return TERN_OK;
+}
+
 tern_status tern_get_device_status(tern_stream_t stream) {
   int dev;
   DeviceState* ds;

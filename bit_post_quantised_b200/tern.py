@@ -26,6 +26,7 @@ EXPORTED = ("tern_packed_bytes", "tern_quantize_pack", "tern_linear", "tern_line
             "tern_linear_act", "tern_linear_epilogue", "tern_linear_batch", "tern_linear_batch_act",
             "tern_linear_batch_epilogue", "tern_linear_strided", "tern_linear_batch_strided",
             "tern_adaln_modulate", "tern_quantize_act_e4m3", "tern_linear_e4m3",
+            "tern_rope_table", "tern_rope", "tern_attention", "tern_gated_residual_norm",
             "tern_dequantize", "tern_get_device_status", "tern_set_wait_limit_ns",
             "tern_selftest_wait_timeout", "tern_status_string", "tern_last_error")
 
@@ -60,8 +61,38 @@ class Epilogue(ctypes.Structure):
                 ("norm_weight", ctypes.c_void_p), ("norm_eps", ctypes.c_float), ("rope_cs", ctypes.c_void_p)]
 
 
+class RopeTensor(ctypes.Structure):
+    """Mirror of tern_rope_tensor."""
+    _fields_ = [("x", ctypes.c_void_p), ("y", ctypes.c_void_p)] + [
+        (n, ctypes.c_int64) for n in ("heads", "x_b", "x_l", "x_h", "y_b", "y_l", "y_h")]
+
+
+class AttentionArgs(ctypes.Structure):
+    """Mirror of tern_attention_args."""
+    _fields_ = [(n, ctypes.c_void_p) for n in ("q", "k", "v", "o")] + [
+        (n, ctypes.c_int64) for n in ("B", "Lq", "Lk", "H", "Hkv", "D", "q_b", "q_l", "q_h", "k_b", "k_l", "k_h",
+                                      "v_b", "v_l", "v_h", "o_b", "o_l", "o_h")] + [
+        ("scale", ctypes.c_float), ("kv_len", ctypes.c_void_p), ("key_mask", ctypes.c_void_p),
+        ("mask_ld", ctypes.c_int64)]
+
+
+class GatedResidualNormArgs(ctypes.Structure):
+    """Mirror of tern_gated_residual_norm_args."""
+    _fields_ = [(n, ctypes.c_void_p) for n in ("x", "o", "x_out", "h")] + [
+        (n, ctypes.c_int64) for n in ("M", "K", "ld_x", "ld_o", "ld_x_out", "ld_h")] + [
+        ("residual_scale", ctypes.c_float), ("post_norm", ctypes.c_int), ("post_weight", ctypes.c_void_p),
+        ("post_eps", ctypes.c_float), ("gate", ctypes.c_void_p), ("gate_tanh", ctypes.c_int),
+        ("pre_norm", ctypes.c_int), ("pre_weight", ctypes.c_void_p), ("pre_eps", ctypes.c_float),
+        ("scale", ctypes.c_void_p), ("shift", ctypes.c_void_p), ("mod_ld", ctypes.c_int64),
+        ("tokens_per_row", ctypes.c_int64)]
+
+
 ACT_NONE = 0       # tern_act values
 ACT_GELU_TANH = 1
+
+NORM_NONE = 0      # tern_norm values
+NORM_RMS = 1
+NORM_LAYER = 2
 
 
 def library_path() -> str:
@@ -107,6 +138,14 @@ def lib() -> ctypes.CDLL:
         L.tern_quantize_act_e4m3.restype = st
         L.tern_linear_e4m3.argtypes = [vp, vp, i64, i64, vp, vp, vp, i64, vp, vp]
         L.tern_linear_e4m3.restype = st
+        L.tern_rope_table.argtypes = [vp, i64, ctypes.c_int, ctypes.POINTER(ctypes.c_int), ctypes.c_double, vp, vp]
+        L.tern_rope_table.restype = st
+        L.tern_rope.argtypes = [ctypes.POINTER(RopeTensor), ctypes.c_int, i64, i64, i64, vp, i64, i64, ctypes.c_int, vp]
+        L.tern_rope.restype = st
+        L.tern_attention.argtypes = [ctypes.POINTER(AttentionArgs), vp]
+        L.tern_attention.restype = st
+        L.tern_gated_residual_norm.argtypes = [ctypes.POINTER(GatedResidualNormArgs), vp]
+        L.tern_gated_residual_norm.restype = st
         L.tern_dequantize.argtypes = [vp, vp, i64, i64, vp, vp]
         L.tern_dequantize.restype = st
         L.tern_get_device_status.argtypes = [vp]
@@ -382,6 +421,189 @@ def linear_batch_strided(problems: Sequence[dict], stream=None) -> None:
         args[i] = _strided_args(p)
         epis[i] = _epilogue(p, strided=True)
     _check(lib().tern_linear_batch_strided(args, epis, len(problems), _stream(stream)))
+
+
+def _launch_on(ts, stream) -> None:
+    """The library launches on the current device: every tensor has to live
+    there.  With a stream other than the current one, the caching allocator
+    is told that the tensors are in use on it."""
+    dev = torch.cuda.current_device() if torch.cuda.is_available() else None
+    for t in ts:
+        if t is not None and (not t.is_cuda or t.device.index != dev):
+            raise ValueError(f"every tensor must be on the current CUDA device ({dev}); got one on {t.device}")
+    if stream is not None:
+        if stream.device.index != dev:
+            raise ValueError(f"the stream belongs to device {stream.device.index}, the current one is {dev}")
+        if stream != torch.cuda.current_stream():
+            for t in ts:
+                if t is not None:
+                    t.record_stream(stream)
+
+
+def _bf16(name: str, t: torch.Tensor, dims) -> None:
+    if t.dtype != torch.bfloat16 or t.dim() not in dims or (t.shape[-1] > 1 and t.stride(-1) != 1):
+        raise ValueError(f"{name} must be bf16 with {' or '.join(map(str, dims))} dimensions and adjacent channels; got "
+                         f"{t.dtype}, shape {tuple(t.shape)}, strides {t.stride()}")
+
+
+def rope_table(ids: torch.Tensor, axes: Sequence[int], theta: float = 10000.0, out: Optional[torch.Tensor] = None,
+               stream=None) -> torch.Tensor:
+    """tern_rope_table: fp32 [L, P, 2] (cos, sin) of token positions ids fp32
+    [L, len(axes)], P = sum(axes) / 2: axis a owns axes[a] channels, pair i of
+    it turning by ids[:, a] * theta^(-2 i / axes[a]).  The table that `rope`
+    and (with P = 64) the linears' rope_cs take."""
+    n = len(axes)
+    if ids.dtype != torch.float32 or ids.dim() != 2 or ids.shape[1] != n or not ids.is_contiguous():
+        raise ValueError(f"ids must be contiguous fp32 [L, {n}], got {ids.dtype} {tuple(ids.shape)}")
+    L, P = ids.shape[0], sum(axes) // 2
+    if out is None:
+        _launch_on((ids,), stream)
+        out = _empty(L, P, 2, dtype=torch.float32, device=ids.device, stream=stream)
+    else:
+        if out.dtype != torch.float32 or out.shape != (L, P, 2) or not out.is_contiguous():
+            raise ValueError(f"out must be contiguous fp32 [{L}, {P}, 2]")
+        _launch_on((ids, out), stream)
+    _check(lib().tern_rope_table(_ptr(ids), L, n, (ctypes.c_int * max(n, 1))(*axes), float(theta), _ptr(out),
+                                 _stream(stream)))
+    return out
+
+
+def rope(xs: Sequence[torch.Tensor], cs: torch.Tensor, halves: bool = False,
+         outs: Optional[Sequence[torch.Tensor]] = None, stream=None):
+    """tern_rope: the heads of up to four bf16 tensors [L, H, D] (or all
+    [B, L, H, D]) of the same tokens, any strides with adjacent channels,
+    rotated by cs fp32 [L, P, 2] (or [B * L, P, 2]): channels 2j and 2j + 1, or
+    with `halves` j and P + j, turn by pair j; channels from 2P on are copied.
+    Returns the rotated tensors (new and contiguous, or `outs`; an element of
+    `outs` may be its input)."""
+    if not xs:
+        return []
+    shape = xs[0].shape
+    for x in xs:
+        _bf16("x", x, (3, 4))
+        if x.dim() != len(shape) or x.shape[:-2] != shape[:-2] or x.shape[-1] != shape[-1]:
+            raise ValueError("the tensors must share their tokens and head size")
+    if cs.dtype != torch.float32 or cs.dim() != 3 or cs.shape[2] != 2 or not cs.is_contiguous():
+        raise ValueError("cs must be contiguous fp32 [rows, P, 2]")
+    _launch_on((*xs, cs, *(outs or ())), stream)
+    if outs is None:
+        outs = [_empty(*x.shape, dtype=x.dtype, device=x.device, stream=stream) for x in xs]
+    elif len(outs) != len(xs):
+        raise ValueError("one output per tensor")
+    arr = (RopeTensor * len(xs))()
+    for i, (x, y) in enumerate(zip(xs, outs)):
+        if y.shape != x.shape:
+            raise ValueError("an output has its input's shape")
+        _bf16("out", y, (3, 4))
+        sx, sy = x.stride(), y.stride()
+        arr[i] = RopeTensor(x.data_ptr(), y.data_ptr(), x.shape[-2], sx[0] if len(sx) == 4 else 0, sx[-3], sx[-2],
+                            sy[0] if len(sy) == 4 else 0, sy[-3], sy[-2])
+    B, L = (shape[0], shape[1]) if len(shape) == 4 else (1, shape[0])
+    _check(lib().tern_rope(arr, len(xs), B, L, shape[-1], _ptr(cs), cs.shape[0], cs.shape[1], 1 if halves else 0,
+                           _stream(stream)))
+    return list(outs)
+
+
+def attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, scale: Optional[float] = None,
+              kv_len: Optional[torch.Tensor] = None, key_mask: Optional[torch.Tensor] = None,
+              out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """tern_attention: softmax(scale q k^T) v of q bf16 [B, Lq, H, D] to k, v
+    bf16 [B, Lk, Hkv, D] (or all without B), any strides with adjacent
+    channels; H / Hkv query heads share a key-value head; scale defaults to
+    1 / sqrt(D).  kv_len int32 [B] and key_mask bool or uint8 [B, Lk] (without
+    B: [1] and [Lk]) say which keys count; a batch entry without one gives
+    zeros.  Returns [B, Lq, H, D] (contiguous, or `out`)."""
+    nd = q.dim()
+    for name, t in (("q", q), ("k", k), ("v", v)):
+        _bf16(name, t, (3, 4))
+        if t.dim() != nd:
+            raise ValueError("q, k and v must all have a batch dimension, or none")
+    B, (Lq, H, D), (Lk, Hkv) = (q.shape[0] if nd == 4 else 1), q.shape[-3:], k.shape[-3:-1]
+    if k.shape != v.shape or k.shape[-1] != D or (nd == 4 and k.shape[0] != B):
+        raise ValueError(f"q {tuple(q.shape)}, k {tuple(k.shape)} and v {tuple(v.shape)} do not fit")
+    if kv_len is not None and (kv_len.dtype != torch.int32 or kv_len.shape != (B,) or not kv_len.is_contiguous()):
+        raise ValueError(f"kv_len must be contiguous int32 [{B}]")
+    mask_ld = 0
+    if key_mask is not None:
+        if (key_mask.dtype not in (torch.bool, torch.uint8) or key_mask.shape != ((B, Lk) if nd == 4 else (Lk,))
+                or (Lk > 1 and key_mask.stride(-1) != 1)):
+            raise ValueError(f"key_mask must be bool or uint8 {'[B, Lk]' if nd == 4 else '[Lk]'} with adjacent keys")
+        mask_ld = key_mask.stride(0) if nd == 4 else 0
+    _launch_on((q, k, v, kv_len, key_mask, out), stream)
+    if out is None:
+        out = _empty(*q.shape, dtype=q.dtype, device=q.device, stream=stream)
+    else:
+        _bf16("out", out, (nd,))
+        if out.shape != q.shape:
+            raise ValueError("out has q's shape")
+    sq, sk, sv, so = (t.stride() for t in (q, k, v, out))
+    if nd == 3:
+        sq, sk, sv, so = ((0, *s) for s in (sq, sk, sv, so))
+    a = AttentionArgs(q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(), B, Lq, Lk, H, Hkv, D, *sq[:3], *sk[:3],
+                      *sv[:3], *so[:3], D ** -0.5 if scale is None else scale,
+                      None if kv_len is None else kv_len.data_ptr(),
+                      None if key_mask is None else key_mask.data_ptr(), mask_ld)
+    _check(lib().tern_attention(ctypes.byref(a), _stream(stream)))
+    return out
+
+
+def gated_residual_norm(x: torch.Tensor, o: torch.Tensor, *, gate: Optional[torch.Tensor] = None,
+                        gate_tanh: bool = False, residual_scale: float = 1.0, post_norm: int = NORM_NONE,
+                        post_weight: Optional[torch.Tensor] = None, post_eps: float = 1e-6, pre_norm: int = NORM_NONE,
+                        pre_weight: Optional[torch.Tensor] = None, pre_eps: float = 1e-6,
+                        scale: Optional[torch.Tensor] = None, shift: Optional[torch.Tensor] = None,
+                        tokens_per_row: Optional[int] = None, x_out: Optional[torch.Tensor] = None,
+                        h: Optional[torch.Tensor] = None, stream=None):
+    """tern_gated_residual_norm: r = residual_scale * x + gate * post(o) per
+    token row of x, o bf16 [M, K], stored to x_out, and h = pre(r) * (1 +
+    scale) + shift.  gate, scale and shift are bf16 [G, K] (or [K]) rows
+    equally far apart, row m // tokens_per_row each (default: row 0 for all),
+    e.g. slices of a modulation output; the norms are NORM_* values.  x_out
+    may be x, h may be o (or the reverse).  Returns (x_out, h); h is None, and
+    not computed, where neither a pre norm, scale and shift, nor h is given."""
+    _bf16("x", x, (2,))
+    _bf16("o", o, (2,))
+    M, K = x.shape
+    if o.shape != x.shape:
+        raise ValueError("x and o must have one shape")
+    T = max(M, 1) if tokens_per_row is None else int(tokens_per_row)
+    G = -(-M // T) if T > 0 else 0
+    mod_ld = K
+    mods = [(n, t) for n, t in (("gate", gate), ("scale", scale), ("shift", shift)) if t is not None]
+    for name, t in mods:
+        _bf16(name, t, (1, 2))
+        if t.shape[-1] != K or (t.shape[0] if t.dim() == 2 else 1) < G:
+            raise ValueError(f"{name} holds fewer than the {G} modulation rows of {K} values that {M} rows at {T} tokens "
+                             "per row need")
+    if G > 1:
+        mod_ld = mods[0][1].stride(0) if mods else K
+        if any(t.stride(0) != mod_ld for _, t in mods):
+            raise ValueError("gate, scale and shift rows must be the same distance apart")
+    for name, t in (("post_weight", post_weight), ("pre_weight", pre_weight)):
+        if t is not None:
+            _bf16(name, t, (1,))
+            if t.shape[0] != K:
+                raise ValueError(f"{name} must hold {K} values")
+    for name, t in (("x_out", x_out), ("h", h)):
+        if t is not None:
+            _bf16(name, t, (2,))
+            if t.shape != x.shape:
+                raise ValueError(f"{name} has x's shape")
+    _launch_on((x, o, gate, scale, shift, post_weight, pre_weight, x_out, h), stream)
+    if x_out is None:
+        x_out = _empty(M, K, dtype=x.dtype, device=x.device, stream=stream)
+    if h is None and (pre_norm != NORM_NONE or scale is not None or shift is not None):
+        h = _empty(M, K, dtype=x.dtype, device=x.device, stream=stream)
+    ld = lambda t: K if t is None or M <= 1 else t.stride(0)  # noqa: E731
+    a = GatedResidualNormArgs(x.data_ptr(), o.data_ptr(), x_out.data_ptr(), None if h is None else h.data_ptr(), M, K,
+                              ld(x), ld(o), ld(x_out), ld(h), residual_scale, post_norm,
+                              None if post_weight is None else post_weight.data_ptr(), post_eps,
+                              None if gate is None else gate.data_ptr(), 1 if gate_tanh else 0, pre_norm,
+                              None if pre_weight is None else pre_weight.data_ptr(), pre_eps,
+                              None if scale is None else scale.data_ptr(), None if shift is None else shift.data_ptr(),
+                              mod_ld, T)
+    _check(lib().tern_gated_residual_norm(ctypes.byref(a), _stream(stream)))
+    return x_out, h
 
 
 def dequantize(packed: torch.Tensor, scales: torch.Tensor, K: int, out: Optional[torch.Tensor] = None,

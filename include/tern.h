@@ -358,6 +358,145 @@ TERN_API tern_status tern_linear_e4m3(const void* xq, const float* a, int64_t M,
                                       const float* scales, const void* bias_bf16, int64_t N, void* y_bf16,
                                       tern_stream_t stream);
 
+/*
+ * Operators of a transformer block between its linears.  The pages describe
+ * nothing there (Section 3.1 names the linears only): these are interface
+ * choices of this library.  bf16 in and out, fp32 (or better) inside, one
+ * rounding per output.  No workspace, one launch each; strides are in
+ * elements.
+ */
+
+/*
+ * Rotary table of several axes (time, height, width, ...).  Axis a of n_axes
+ * owns axis_dims[a] consecutive channels (even, >= 2), that is axis_dims[a] / 2
+ * channel pairs; pair i of axis a of token m turns by
+ *     ids[m, a] * theta^(-2 i / axis_dims[a])     (64-bit angle),
+ * and cs[m] holds (cos, sin) of its P = sum(axis_dims) / 2 pairs in order:
+ * with P = 64 the table that tern_epilogue's rope_cs takes.
+ *   ids   [L, n_axes] fp32 positions (4-byte aligned), whole or not, |angle| < 2^31;
+ *         a position that is not finite gives NaN.
+ *   cs    [L, P, 2] fp32, written (8-byte aligned), not overlapping ids.
+ * 1 <= n_axes <= 4, P <= 128 (TERN_ERR_UNSUPPORTED_SHAPE), theta > 0 and
+ * finite; axis_dims is host memory.  L == 0 is a no-op.
+ */
+TERN_API tern_status tern_rope_table(const float* ids, int64_t L, int n_axes, const int* axis_dims, double theta,
+                                     float* cs, tern_stream_t stream);
+
+/* Which channels of a head form pair j of its 2P rotated channels. */
+typedef enum {
+  TERN_ROPE_PAIRS = 0, /* 2j and 2j + 1 */
+  TERN_ROPE_HALVES = 1 /* j and P + j */
+} tern_rope_layout;
+
+/* One tensor of heads for tern_rope: x and y [B, L, heads, head_dim]. */
+typedef struct {
+  const void* x;
+  void* y;                    /* x itself (with x's strides: in place) or not overlapping it */
+  int64_t heads;
+  int64_t x_b, x_l, x_h;      /* elements between batch entries, tokens and heads of x */
+  int64_t y_b, y_l, y_h;
+} tern_rope_tensor;
+
+/*
+ * Rotates the heads of up to four tensors of the same tokens (q and k) by one
+ * table: channels (a, b) of pair j become (a cos - b sin, a sin + b cos);
+ * channels from 2P on are copied.
+ *   cs       [cs_rows, P, 2] fp32 (16-byte aligned): a row per token, shared by
+ *            the batch (cs_rows = L), or a row per batch entry and token
+ *            (cs_rows = B * L).
+ *   P, head_dim  2P % 16 == 0, 2P <= head_dim, head_dim % 8 == 0, head_dim <= 256.
+ * x and y 16-byte aligned, every stride a multiple of 8 (0 allowed in x), the
+ * elements of y distinct: y's strides nest, in either order of tokens and
+ * heads, inside its batch stride.  B, L >= 0 and heads >= 0; none is a no-op.
+ * No y overlaps another tensor's x or y, or the table: regions are compared
+ * by their spans, unless they share their strides and lie in different
+ * channels or heads of one parent's rows.
+ */
+TERN_API tern_status tern_rope(const tern_rope_tensor* tensors, int count, int64_t B, int64_t L, int64_t head_dim,
+                               const float* cs, int64_t cs_rows, int64_t P, int layout, tern_stream_t stream);
+
+/*
+ * Attention of queries to an encoder's states (or to any keys and values):
+ *     o[b, l, h] = sum_j softmax_j(scale * q[b, l, h] . k[b, j, h']) v[b, j, h'],
+ * h' = h / (H / Hkv), over the valid keys j < kv_len[b] with key_mask[b, j]
+ * != 0.  A batch entry without a valid key gives zeros.  What masked keys and
+ * values hold (infinities and NaN too) does not reach the output; scores that
+ * are NaN, or infinite at their row's maximum, give NaN rows.
+ *   q, o      [B, Lq, H, D];  k, v  [B, Lk, Hkv, D]; channels are adjacent.
+ *   kv_len    [B] int32 device memory or NULL (all Lk); clamped to [0, Lk].
+ *   key_mask  [B, Lk] bytes device memory, rows mask_ld apart, or NULL.
+ * H % Hkv == 0, D % 8 == 0, 8 <= D <= 128, Lq, Lk < 2^30 and B * H < 2^20
+ * (TERN_ERR_UNSUPPORTED_SHAPE); pointers 16-byte aligned, strides multiples
+ * of 8 below 2^38, 0 allowed in q, k and v (a broadcast); the elements of o
+ * are distinct (strides as tern_rope's y) and o overlaps no input.  scale > 0
+ * and finite.  B, Lq or H == 0 is a no-op; Lk == 0 writes zeros (k and v may
+ * be NULL).
+ */
+typedef struct {
+  const void *q, *k, *v;
+  void* o;
+  int64_t B, Lq, Lk, H, Hkv, D;
+  int64_t q_b, q_l, q_h; /* elements between batch entries, tokens and heads */
+  int64_t k_b, k_l, k_h;
+  int64_t v_b, v_l, v_h;
+  int64_t o_b, o_l, o_h;
+  float scale;
+  const int32_t* kv_len;
+  const uint8_t* key_mask;
+  int64_t mask_ld;
+} tern_attention_args;
+
+TERN_API tern_status tern_attention(const tern_attention_args* args, tern_stream_t stream);
+
+/* Normalisation of a row v of K channels (tern_gated_residual_norm). */
+typedef enum {
+  TERN_NORM_NONE = 0,
+  TERN_NORM_RMS = 1,   /* v / sqrt(mean(v^2) + eps) */
+  TERN_NORM_LAYER = 2  /* (v - mean(v)) / sqrt(var(v) + eps), biased variance */
+} tern_norm;
+
+/*
+ * The gated residual update of a block's output o with the norm of o before
+ * it and the norm of the updated stream after it, per token row m with
+ * g = m / tokens_per_row:
+ *     r        = residual_scale * x[m] + gate'[g] * post(o[m]) * post_weight
+ *     x_out[m] = r
+ *     h[m]     = pre(r) * pre_weight * (1 + scale[g]) + shift[g]
+ * gate' = gate, or tanh(gate) with gate_tanh != 0; a NULL gate or weight is 1.
+ * Both outputs come from the fp32 r (h not from the rounded x_out).
+ *   x, o      [M, K] bf16, rows ld_x and ld_o elements apart.
+ *   x_out, h  [M, K] bf16, rows ld_x_out and ld_h apart, written.  h may be NULL
+ *             (the update alone).  An output may be x or o itself, row for row
+ *             (the same pointer and row stride); no other overlap of an output
+ *             with an input or the other output.
+ *   gate, scale, shift  ceil(M / tokens_per_row) rows of K bf16, mod_ld apart,
+ *             scale and shift both given or both NULL; 16-byte aligned.
+ *   post_weight, pre_weight  [K] bf16 or NULL, 16-byte aligned.
+ * K % 8 == 0 and 8 <= K <= 16384, M < 2^31, tokens_per_row >= 1
+ * (TERN_ERR_UNSUPPORTED_SHAPE); row strides >= K and multiples of 8; eps of a
+ * requested norm finite and >= 0.  M == 0 is a no-op.
+ */
+typedef struct {
+  const void *x, *o;
+  void *x_out, *h;
+  int64_t M, K;
+  int64_t ld_x, ld_o, ld_x_out, ld_h;
+  float residual_scale;
+  int post_norm; /* tern_norm of o */
+  const void* post_weight;
+  float post_eps;
+  const void* gate;
+  int gate_tanh;
+  int pre_norm; /* tern_norm of the updated stream */
+  const void* pre_weight;
+  float pre_eps;
+  const void *scale, *shift;
+  int64_t mod_ld;
+  int64_t tokens_per_row;
+} tern_gated_residual_norm_args;
+
+TERN_API tern_status tern_gated_residual_norm(const tern_gated_residual_norm_args* args, tern_stream_t stream);
+
 /* Synchronises `stream`, then returns and clears the device status word of the
  * current device: TERN_ERR_TIMEOUT if any kernel's bounded wait ran out since
  * the last call, else TERN_ERR_LAUNCH_CONFIG if a kernel refused an
