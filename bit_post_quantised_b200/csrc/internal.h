@@ -190,6 +190,7 @@ cudaError_t launch_gated_residual_norm(const ResNormArgs& a, cudaStream_t stream
 
 // Attention of q [B, Lq, H, D] to k, v [B, Lk, Hkv, D] (strides in elements).
 constexpr int kAttnMaxD = 128;
+constexpr int kAttnRowsMax = 64;  // packed query rows of a key-value head up to which the row kernel runs
 struct AttnArgs {
   const uint16_t *q, *k, *v;
   uint16_t* o;
@@ -200,6 +201,18 @@ struct AttnArgs {
   int B, Lq, Lk, H, Hkv, D;
   float scale_log2;         // softmax scale * log2(e)
 };
+// The same with the tensor maps {D, L, H, B} (box {64, 128, 1, 1}, 128-byte
+// swizzle) that the tile kernel loads through; q_h ... are 0 for a dimension
+// that the map has once (a broadcast), else 1.
+struct alignas(64) AttnTileArgs {
+  CUtensorMap tq, tk, tv;
+  AttnArgs a;
+  int q_b, q_h, k_b, k_h, v_b, v_h;
+  int pairs;  // of 128-row query tiles
+  unsigned long long wait_limit_ns;
+  unsigned int* status;
+};
+cudaError_t launch_attention_tile(const AttnTileArgs& t, cudaStream_t stream);
 // One read of k and v for up to 16 packed query rows; see attention_rows.cu.
 cudaError_t launch_attention_rows(const AttnArgs& a, int sms, cudaStream_t stream);
 

@@ -966,6 +966,27 @@ bool overlaps_flat(const Heads& t, const void* p, size_t bytes) {
   return !t.empty() && overlaps(t.p, size_t(t.span()) * 2, p, bytes);
 }
 
+// t as a 4-D map {D, L, H, B} whose box is 64 channels of 128 tokens; channels
+// past D and tokens past L read as zero.  A dimension of stride 0 or size 1
+// is mapped once, and its coordinate's factor (h_mul, b_mul) is 0.
+tern_status make_heads_map(CUtensorMap* map, const Heads& t, int* h_mul, int* b_mul) {
+  EncodeTiledFn enc = encode_fn();
+  if (!enc) return fail(TERN_ERR_CUDA, "cuTensorMapEncodeTiled unavailable");
+  *h_mul = t.H > 1 && t.h != 0;
+  *b_mul = t.B > 1 && t.b != 0;
+  const cuuint64_t dims[4] = {cuuint64_t(t.D), cuuint64_t(t.L), *h_mul ? cuuint64_t(t.H) : 1,
+                              *b_mul ? cuuint64_t(t.B) : 1};
+  const cuuint64_t one = cuuint64_t(t.D) * 2;  // a stride that no coordinate uses
+  const cuuint64_t strides[3] = {t.L > 1 ? cuuint64_t(t.l) * 2 : one, *h_mul ? cuuint64_t(t.h) * 2 : one,
+                                 *b_mul ? cuuint64_t(t.b) * 2 : one};
+  const cuuint32_t box[4] = {64, 128, 1, 1}, estr[4] = {1, 1, 1, 1};
+  CUresult r = enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(t.p), dims, strides, box, estr,
+                   CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  if (r != CUDA_SUCCESS) return fail(TERN_ERR_CUDA, "cuTensorMapEncodeTiled (heads) failed (%d)", int(r));
+  return TERN_OK;
+}
+
 const uint16_t* u16(const void* p) { return static_cast<const uint16_t*>(p); }
 uint16_t* u16w(void* p) { return static_cast<uint16_t*>(p); }
 
@@ -1113,7 +1134,27 @@ tern_status tern_attention(const tern_attention_args* args, tern_stream_t stream
   DeviceState* ds;
   tern_status s;
   if ((s = current_device(&dev, &ds)) != TERN_OK) return s;
-  cudaError_t e = launch_attention_rows(a, ds->sms, reinterpret_cast<cudaStream_t>(stream));
+  // The row kernel reads K and V once per 16 packed query rows; the tile
+  // kernel once per 256 rows of a head.  (A tensor map has no dimension of
+  // stride 0: tokens that are one broadcast row take the row kernel.)
+  const bool flat = (t.Lq > 1 && t.q_l == 0) || (t.Lk > 1 && (t.k_l == 0 || t.v_l == 0));
+  cudaError_t e;
+  if (t.Lq * (t.H / t.Hkv) <= kAttnRowsMax || flat || t.Lk == 0) {
+    e = launch_attention_rows(a, ds->sms, reinterpret_cast<cudaStream_t>(stream));
+  } else {
+    AttnTileArgs ta;
+    std::memset(static_cast<void*>(&ta), 0, sizeof ta);
+    ta.a = a;
+    if ((s = make_heads_map(&ta.tq, q, &ta.q_h, &ta.q_b)) != TERN_OK || (s = make_heads_map(&ta.tk, k, &ta.k_h, &ta.k_b)) != TERN_OK ||
+        (s = make_heads_map(&ta.tv, v, &ta.v_h, &ta.v_b)) != TERN_OK)
+      return s;
+    const int64_t pairs = (t.Lq + 255) / 256;
+    if (pairs * t.B * t.H > INT32_MAX) return fail(TERN_ERR_UNSUPPORTED_SHAPE, "attention: too many query rows");
+    ta.pairs = int(pairs);
+    ta.wait_limit_ns = g_wait_limit_ns.load();
+    ta.status = ds->status;
+    e = launch_attention_tile(ta, reinterpret_cast<cudaStream_t>(stream));
+  }
   if (e != cudaSuccess) return cuda_fail(e, "attention launch");
   return TERN_OK;
 }
