@@ -149,12 +149,12 @@ cudaError_t launch_ternary_fp8(const Batch& batch, int pairs, cudaStream_t strea
 // Rotary table: the frequency and axis of every channel pair.
 constexpr int kRopeMaxPairs = 128;
 struct RopeFreqs {
-  double omega[kRopeMaxPairs];  // theta^(-2 i / d_a)
+  double turns[kRopeMaxPairs];  // theta^(-2 i / d_a), in quarter turns
   uint8_t axis[kRopeMaxPairs];
   int pairs, n_axes;
 };
 // cs [L][pairs][2] from ids [L][n_axes].
-cudaError_t launch_rope_table(const float* ids, long long L, const RopeFreqs& f, float* cs, cudaStream_t stream);
+cudaError_t launch_rope_table(const float* ids, int L, const RopeFreqs& f, float* cs, cudaStream_t stream);
 
 // Rotation of up to kRopeTensors head tensors of the same tokens.
 constexpr int kRopeTensors = 4;

@@ -5,11 +5,14 @@
 // Table: pair j of axis a (d_a channels, d_a / 2 pairs, i = the pair's place
 // on its axis) of token m turns by ids[m, a] * theta^(-2 i / d_a).  Far
 // positions turn by thousands of radians, where one fp32 ulp of the angle is
-// already visible in its cosine, so the angle and its reduction to
-// [-pi/4, pi/4] are in 64 bits.  There the sine and cosine are their Taylor
-// polynomials (degrees 11 and 12: truncation below 7e-12), rounded once to
-// fp32.  One thread owns one pair and walks over tokens, so its frequency
-// stays in registers; stores are 8 bytes per lane, consecutive.
+// already visible in its cosine, so the angle is counted in quarter turns and
+// reduced to [-1/2, 1/2] in 64 bits.  There the sine and cosine are their
+// Taylor polynomials (degrees 11 and 12: truncation below 7e-12), rounded
+// once to fp32.  A lane owns a token and its warp walks over pairs, so the
+// frequency is one constant operand for the warp (a frequency per lane, read
+// from the parameters, serialised 32 constant reads: 21 us for 57,677 tokens
+// of 64 pairs); the block's 32 rows are turned around in shared memory so
+// that stores are consecutive.
 //
 // Rotation: bound by HBM (each element read once, written once).  A thread
 // owns one 16-byte group of channels of a token (or, for half-split pairs,
@@ -26,48 +29,49 @@ namespace {
 
 // ------------------------------------------------------------------- table
 constexpr int kTableThreads = 256;
-constexpr int kTableRows = 4;  // token rows per thread
+constexpr int kTableRows = 32;  // token rows per block, one per lane
 
-// cos and sin of `a`, |a| < 2^31 pi / 2, each rounded to fp32.
-__device__ __forceinline__ float2 cos_sin(double a) {
-  // n = the nearest multiple of pi/2, r = a - n pi/2 (pi/2 as two doubles).
-  const double n = rint(a * 0.63661977236758134308);
-  double r = fma(-n, 1.57079632679489661923, a);
-  r = fma(-n, 6.12323399573676603587e-17, r);
-  const double z = r * r;
-  double s = fma(z, -1.0 / 39916800.0, 1.0 / 362880.0);
-  s = fma(z, s, -1.0 / 5040.0);
-  s = fma(z, s, 1.0 / 120.0);
-  s = fma(z, s, -1.0 / 6.0);
-  s = fma(z * r, s, r);
-  double c = fma(z, 1.0 / 479001600.0, -1.0 / 3628800.0);
-  c = fma(z, c, 1.0 / 40320.0);
-  c = fma(z, c, -1.0 / 720.0);
-  c = fma(z, c, 1.0 / 24.0);
-  c = fma(z, c, -0.5);
-  c = fma(z, c, 1.0);
+// cos and sin of x * w quarter turns, each rounded once to fp32 (|x w| < 2^50).
+__device__ __forceinline__ float2 cos_sin(double x, double w) {
+  // Adding 1.5 * 2^52 leaves the nearest integer n (its low bits count the
+  // quarter turns); the remainder x w - n, in [-1/2, 1/2], is rounded once.
+  const double magic = 6755399441055744.0;
+  const double u = fma(x, w, magic);
+  const int q = __double2loint(u);
+  const double f = fma(x, w, magic - u);
+  const double z = f * f;
+  // sin(pi/2 f) / f and cos(pi/2 f): Taylor coefficients (pi/2)^k / k!, alternating.
+  constexpr double h = 1.57079632679489661923, h2 = h * h;
+  constexpr double s1 = h * h2 / 6, s2 = s1 * h2 / 20, s3 = s2 * h2 / 42, s4 = s3 * h2 / 72, s5 = s4 * h2 / 110;
+  constexpr double c1 = h2 / 2, c2 = c1 * h2 / 12, c3 = c2 * h2 / 30, c4 = c3 * h2 / 56, c5 = c4 * h2 / 90,
+                   c6 = c5 * h2 / 132;
+  const double s = f * fma(z, fma(z, fma(z, fma(z, fma(z, -s5, s4), -s3), s2), -s1), h);
+  const double c = fma(z, fma(z, fma(z, fma(z, fma(z, fma(z, c6, -c5), c4), -c3), c2), -c1), 1.0);
   const float fs = float(s), fc = float(c);
-  const int q = __double2int_rn(n) & 3;  // quarter turns
   const float cc = (q & 1) ? fs : fc, ss = (q & 1) ? fc : fs;
-  return make_float2((q == 1 || q == 2) ? -cc : cc, (q >= 2) ? -ss : ss);
+  // cos changes its sign for quarter turns 1 and 2, sin for 2 and 3.
+  return make_float2(__uint_as_float(__float_as_uint(cc) ^ (uint32_t(q + 1) << 30 & 0x80000000u)),
+                     __uint_as_float(__float_as_uint(ss) ^ (uint32_t(q) << 30 & 0x80000000u)));
 }
 
 __global__ void __launch_bounds__(kTableThreads)
-    rope_table_kernel(const float* __restrict__ ids, long long L, const __grid_constant__ RopeFreqs f, float2* cs) {
+    rope_table_kernel(const float* __restrict__ ids, int L, const __grid_constant__ RopeFreqs f, float2* cs) {
+  extern __shared__ float2 tile[];  // [kTableRows][pairs + 1]: a column of lanes meets every bank
   pdl_wait();
   pdl_trigger();
-  const int P = f.pairs;
-  const int rows = kTableThreads / P;  // token rows side by side
-  const int j = threadIdx.x % P, r = threadIdx.x / P;
-  if (r >= rows) return;
-  const double omega = f.omega[j];
-  const int axis = f.axis[j];
-  const long long m0 = (long long)blockIdx.x * (rows * kTableRows) + r;
+  const int P = f.pairs, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int m0 = int(blockIdx.x) * kTableRows, rows = min(kTableRows, L - m0);
+  double x[4];  // this lane's token
 #pragma unroll
-  for (int t = 0; t < kTableRows; ++t) {
-    const long long m = m0 + t * rows;
-    if (m < L) cs[m * P + j] = cos_sin(double(ids[m * f.n_axes + axis]) * omega);
+  for (int a = 0; a < 4; ++a) x[a] = a < f.n_axes && lane < rows ? double(ids[(long long)(m0 + lane) * f.n_axes + a]) : 0.0;
+  for (int j = warp; j < P; j += kTableThreads / 32) {
+    const int axis = f.axis[j];
+    tile[lane * (P + 1) + j] = cos_sin(axis == 0 ? x[0] : axis == 1 ? x[1] : axis == 2 ? x[2] : x[3], f.turns[j]);
   }
+  __syncthreads();
+  float2* out = cs + (long long)m0 * P;
+  for (int r = warp; r < rows; r += kTableThreads / 32)
+    for (int j = lane; j < P; j += 32) out[r * P + j] = tile[r * (P + 1) + j];
 }
 
 // ---------------------------------------------------------------- rotation
@@ -145,11 +149,10 @@ __global__ void __launch_bounds__(256) rope_kernel(const __grid_constant__ RopeA
 
 }  // namespace
 
-cudaError_t launch_rope_table(const float* ids, long long L, const RopeFreqs& f, float* cs, cudaStream_t stream) {
-  const long long rows = (kTableThreads / f.pairs) * kTableRows;
-  const long long grid = (L + rows - 1) / rows;
-  return launch_pdl(rope_table_kernel, dim3(unsigned(grid)), dim3(kTableThreads), 0, stream, 1, ids, L, f,
-                    reinterpret_cast<float2*>(cs));
+cudaError_t launch_rope_table(const float* ids, int L, const RopeFreqs& f, float* cs, cudaStream_t stream) {
+  const unsigned grid = unsigned((L + kTableRows - 1) / kTableRows);
+  return launch_pdl(rope_table_kernel, dim3(grid), dim3(kTableThreads), kTableRows * (f.pairs + 1) * sizeof(float2), stream,
+                    1, ids, L, f, reinterpret_cast<float2*>(cs));
 }
 
 cudaError_t launch_rope(RopeArgs a, bool halves, cudaStream_t stream) {

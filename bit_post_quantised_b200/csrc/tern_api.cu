@@ -1007,7 +1007,7 @@ tern_status tern_rope_table(const float* ids, int64_t L, int n_axes, const int* 
       return fail(TERN_ERR_UNSUPPORTED_SHAPE, "rope_table: axis sizes are even, >= 2 and at most %d in all (axis %d has %d)",
                   2 * kRopeMaxPairs, a, d);
     for (int i = 0; i < d / 2; ++i) {
-      f.omega[f.pairs] = std::pow(theta, -2.0 * i / d);
+      f.turns[f.pairs] = std::pow(theta, -2.0 * i / d) * 0.63661977236758134308;  // 2 / pi
       f.axis[f.pairs++] = uint8_t(a);
     }
   }
@@ -1021,7 +1021,7 @@ tern_status tern_rope_table(const float* ids, int64_t L, int n_axes, const int* 
   DeviceState* ds;
   tern_status s;
   if ((s = current_device(&dev, &ds)) != TERN_OK) return s;
-  cudaError_t e = launch_rope_table(ids, L, f, cs, reinterpret_cast<cudaStream_t>(stream));
+  cudaError_t e = launch_rope_table(ids, int(L), f, cs, reinterpret_cast<cudaStream_t>(stream));
   if (e != cudaSuccess) return cuda_fail(e, "rope_table launch");
   return TERN_OK;
 }

@@ -172,8 +172,10 @@ def _ptr(t: Optional[torch.Tensor]):
 
 
 def _stream(stream: Optional[torch.cuda.Stream]):
-    s = stream if stream is not None else torch.cuda.current_stream()
-    return ctypes.c_void_p(s.cuda_stream)
+    if stream is not None:
+        return stream.cuda_stream
+    # The handle alone: a torch.cuda.Stream object around it costs 3 us.
+    return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
 
 
 def _empty(*shape, dtype, device, stream=None) -> torch.Tensor:
@@ -183,6 +185,12 @@ def _empty(*shape, dtype, device, stream=None) -> torch.Tensor:
         return torch.empty(*shape, dtype=dtype, device=device)
     with torch.cuda.stream(stream):
         return torch.empty(*shape, dtype=dtype, device=device)
+
+
+def _empty_as(t: torch.Tensor, stream=None) -> torch.Tensor:
+    """A contiguous output buffer of t's shape and type (see _empty)."""
+    return torch.empty_like(t) if stream is None and t.is_contiguous() else _empty(t.shape, dtype=t.dtype,
+                                                                                   device=t.device, stream=stream)
 
 
 def packed_bytes(N: int, K: int) -> int:
@@ -427,11 +435,16 @@ def _launch_on(ts, stream) -> None:
     """The library launches on the current device: every tensor has to live
     there.  With a stream other than the current one, the caching allocator
     is told that the tensors are in use on it."""
-    dev = torch.cuda.current_device() if torch.cuda.is_available() else None
+    dev = -1
     for t in ts:
-        if t is not None and (not t.is_cuda or t.device.index != dev):
-            raise ValueError(f"every tensor must be on the current CUDA device ({dev}); got one on {t.device}")
-    if stream is not None:
+        if t is not None:
+            if not t.is_cuda:
+                raise ValueError(f"every tensor must be on the current CUDA device; got one on {t.device}")
+            if dev < 0:
+                dev = torch.cuda.current_device()
+            if t.get_device() != dev:
+                raise ValueError(f"every tensor must be on the current CUDA device ({dev}); got one on {t.device}")
+    if stream is not None and dev >= 0:
         if stream.device.index != dev:
             raise ValueError(f"the stream belongs to device {stream.device.index}, the current one is {dev}")
         if stream != torch.cuda.current_stream():
@@ -441,7 +454,7 @@ def _launch_on(ts, stream) -> None:
 
 
 def _bf16(name: str, t: torch.Tensor, dims) -> None:
-    if t.dtype != torch.bfloat16 or t.dim() not in dims or (t.shape[-1] > 1 and t.stride(-1) != 1):
+    if t.dtype is not torch.bfloat16 or t.dim() not in dims or (t.stride(-1) != 1 and t.shape[-1] > 1):
         raise ValueError(f"{name} must be bf16 with {' or '.join(map(str, dims))} dimensions and adjacent channels; got "
                          f"{t.dtype}, shape {tuple(t.shape)}, strides {t.stride()}")
 
@@ -487,7 +500,7 @@ def rope(xs: Sequence[torch.Tensor], cs: torch.Tensor, halves: bool = False,
         raise ValueError("cs must be contiguous fp32 [rows, P, 2]")
     _launch_on((*xs, cs, *(outs or ())), stream)
     if outs is None:
-        outs = [_empty(*x.shape, dtype=x.dtype, device=x.device, stream=stream) for x in xs]
+        outs = [_empty_as(x, stream) for x in xs]
     elif len(outs) != len(xs):
         raise ValueError("one output per tensor")
     arr = (RopeTensor * len(xs))()
@@ -531,7 +544,7 @@ def attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, scale: Optional
         mask_ld = key_mask.stride(0) if nd == 4 else 0
     _launch_on((q, k, v, kv_len, key_mask, out), stream)
     if out is None:
-        out = _empty(*q.shape, dtype=q.dtype, device=q.device, stream=stream)
+        out = _empty_as(q, stream)
     else:
         _bf16("out", out, (nd,))
         if out.shape != q.shape:
@@ -591,9 +604,9 @@ def gated_residual_norm(x: torch.Tensor, o: torch.Tensor, *, gate: Optional[torc
                 raise ValueError(f"{name} has x's shape")
     _launch_on((x, o, gate, scale, shift, post_weight, pre_weight, x_out, h), stream)
     if x_out is None:
-        x_out = _empty(M, K, dtype=x.dtype, device=x.device, stream=stream)
+        x_out = _empty_as(x, stream)
     if h is None and (pre_norm != NORM_NONE or scale is not None or shift is not None):
-        h = _empty(M, K, dtype=x.dtype, device=x.device, stream=stream)
+        h = _empty_as(x, stream)
     ld = lambda t: K if t is None or M <= 1 else t.stride(0)  # noqa: E731
     a = GatedResidualNormArgs(x.data_ptr(), o.data_ptr(), x_out.data_ptr(), None if h is None else h.data_ptr(), M, K,
                               ld(x), ld(o), ld(x_out), ld(h), residual_scale, post_norm,
