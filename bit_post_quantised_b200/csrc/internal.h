@@ -167,13 +167,11 @@ struct RopeTensor {
 struct RopeArgs {
   RopeTensor t[kRopeTensors];  // unused ones have no heads
   const float* cs;
-  long long rows, L;  // rows = batch * L
-  int heads;          // of all tensors
+  int rows, L;        // rows = batch * L
   int head_dim, rot;
   int cs_per_batch;   // the table has a row per (batch entry, token), not per token
-  int units, turned_units, heads_par, rows_par;  // set by launch_rope
 };
-cudaError_t launch_rope(RopeArgs a, bool halves, cudaStream_t stream);
+cudaError_t launch_rope(const RopeArgs& a, bool halves, cudaStream_t stream);
 
 // Gated residual update with the norms around it; rows of K elements, K % 8 == 0.
 constexpr int kNormNone = 0, kNormRms = 1, kNormLayer = 2;

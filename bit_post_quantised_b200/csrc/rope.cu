@@ -15,10 +15,9 @@
 // that stores are consecutive.
 //
 // Rotation: bound by HBM (each element read once, written once).  A thread
-// owns one 16-byte group of channels of a token (or, for half-split pairs,
-// the two groups that turn together) and walks over the heads of q and k, so
-// the table, shared by all heads, is read once per token and stays in
-// registers.  fp32 products, one rounding to bf16.
+// owns 16 bytes of channels of a token (for half-split pairs 8 bytes of each
+// half: the same four pairs) and walks over heads, so the table, shared by
+// all heads, stays in registers.  fp32 products, one rounding to bf16.
 #include "internal.h"
 #include "kernel_common.cuh"
 #include "ptx.cuh"
@@ -88,61 +87,77 @@ __device__ __forceinline__ uint32_t turn(uint32_t w, float c, float s) {
   return pack2(a * c - b * s, a * s + b * c);
 }
 
-// Threads of a block: slot = tid / units owns (token row of the block, first
-// head), unit = tid % units one group of channels; both fixed, so the table
-// entries stay in registers while the thread walks over heads.
+constexpr int kBatch = 4;  // heads a thread has in flight
+
+// threadIdx.x is the group of channels, .y the first head, .z the token row of
+// the block; blockIdx.y the tensor.  The table's entries stay in registers
+// while the thread walks over heads; its loads of kBatch heads are issued
+// before the first store (x may be y, so the compiler cannot move them).
 template <bool HALVES>
 __global__ void __launch_bounds__(256) rope_kernel(const __grid_constant__ RopeArgs a) {
   pdl_wait();
   pdl_trigger();
-  const int unit = threadIdx.x % a.units, slot = threadIdx.x / a.units;
-  const int row = slot / a.heads_par, h0 = slot - row * a.heads_par;
-  const long long m = (long long)blockIdx.x * a.rows_par + row;
-  if (row >= a.rows_par || m >= a.rows) return;
-  const long long b = m / a.L, l = m - b * a.L;
-  const bool turned = unit < a.turned_units;
-  // First channel of this thread's group; half-split: of its first half.
-  const int c0 = turned ? 8 * unit : (HALVES ? a.rot + 8 * (unit - a.turned_units) : 8 * unit);
-  constexpr int NC = HALVES ? 8 : 4;  // pairs per thread
-  float c[NC], s[NC];
+  const int unit = threadIdx.x;
+  const unsigned m = blockIdx.x * blockDim.z + threadIdx.z;
+  if (m >= unsigned(a.rows)) return;
+  const unsigned b = a.L == a.rows ? 0u : m / unsigned(a.L), l = m - b * unsigned(a.L);
+  const bool turned = unit < a.rot / 8;
+  // First channel of this thread's 16 bytes; half-split: of 8 bytes in each half.
+  const int c0 = HALVES && turned ? 4 * unit : 8 * unit;
+  const int c1 = HALVES && turned ? a.rot / 2 + 4 * unit : 8 * unit + 4;
+  float4 cs[2];  // (cos, sin) of four pairs
   if (turned) {
-    const float4* t = reinterpret_cast<const float4*>(a.cs + ((a.cs_per_batch ? m : l) * (a.rot / 2) + NC * unit) * 2);
-#pragma unroll
-    for (int i = 0; i < NC / 2; ++i) {
-      const float4 v = __ldg(t + i);
-      c[2 * i] = v.x, s[2 * i] = v.y, c[2 * i + 1] = v.z, s[2 * i + 1] = v.w;
-    }
+    const float4* t = reinterpret_cast<const float4*>(a.cs + ((long long)(a.cs_per_batch ? m : l) * (a.rot / 2) + 4 * unit) * 2);
+    cs[0] = __ldg(t);
+    cs[1] = __ldg(t + 1);
   }
-#pragma unroll 4
-  for (int hh = h0; hh < a.heads; hh += a.heads_par) {
-    int t = 0, h = hh;
+  const RopeTensor& T = a.t[blockIdx.y];
+  const uint16_t* const x = T.x + b * T.x_b + l * T.x_l;
+  uint16_t* const y = T.y + b * T.y_b + l * T.y_l;
+  for (int h0 = threadIdx.y; h0 < T.heads; h0 += kBatch * blockDim.y) {
+    uint2 v[kBatch], w[kBatch];
 #pragma unroll
-    for (int i = 0; i + 1 < kRopeTensors; ++i)
-      if (t == i && h >= a.t[i].heads) h -= a.t[i].heads, t = i + 1;
-    const RopeTensor& T = a.t[t];
-    const uint16_t* x = T.x + b * T.x_b + l * T.x_l + h * T.x_h + c0;
-    uint16_t* y = T.y + b * T.y_b + l * T.y_l + h * T.y_h + c0;
-    uint4 v = *reinterpret_cast<const uint4*>(x);
-    if (!turned) {
-      *reinterpret_cast<uint4*>(y) = v;
-    } else if constexpr (!HALVES) {
-      v.x = turn(v.x, c[0], s[0]);
-      v.y = turn(v.y, c[1], s[1]);
-      v.z = turn(v.z, c[2], s[2]);
-      v.w = turn(v.w, c[3], s[3]);
-      *reinterpret_cast<uint4*>(y) = v;
-    } else {
-      uint4 w = *reinterpret_cast<const uint4*>(x + a.rot / 2);
-      uint32_t* pv = &v.x;
-      uint32_t* pw = &w.x;
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const float a0 = lo_f(pv[i]), a1 = hi_f(pv[i]), b0 = lo_f(pw[i]), b1 = hi_f(pw[i]);
-        pv[i] = pack2(a0 * c[2 * i] - b0 * s[2 * i], a1 * c[2 * i + 1] - b1 * s[2 * i + 1]);
-        pw[i] = pack2(a0 * s[2 * i] + b0 * c[2 * i], a1 * s[2 * i + 1] + b1 * c[2 * i + 1]);
+    for (int i = 0; i < kBatch; ++i) {
+      const int h = h0 + i * blockDim.y;
+      if (h < T.heads) {
+        const uint16_t* p = x + h * T.x_h;
+        if constexpr (HALVES) {
+          v[i] = *reinterpret_cast<const uint2*>(p + c0);
+          w[i] = *reinterpret_cast<const uint2*>(p + c1);
+        } else {
+          const uint4 q = *reinterpret_cast<const uint4*>(p + c0);
+          v[i] = make_uint2(q.x, q.y), w[i] = make_uint2(q.z, q.w);
+        }
       }
-      *reinterpret_cast<uint4*>(y) = v;
-      *reinterpret_cast<uint4*>(y + a.rot / 2) = w;
+    }
+#pragma unroll
+    for (int i = 0; i < kBatch; ++i) {
+      const int h = h0 + i * blockDim.y;
+      if (h < T.heads) {
+        uint16_t* p = y + h * T.y_h;
+        uint2 r0 = v[i], r1 = w[i];
+        if (turned) {
+          if constexpr (HALVES) {
+            const float a0 = lo_f(r0.x), a1 = hi_f(r0.x), a2 = lo_f(r0.y), a3 = hi_f(r0.y);
+            const float b0 = lo_f(r1.x), b1 = hi_f(r1.x), b2 = lo_f(r1.y), b3 = hi_f(r1.y);
+            r0.x = pack2(a0 * cs[0].x - b0 * cs[0].y, a1 * cs[0].z - b1 * cs[0].w);
+            r0.y = pack2(a2 * cs[1].x - b2 * cs[1].y, a3 * cs[1].z - b3 * cs[1].w);
+            r1.x = pack2(a0 * cs[0].y + b0 * cs[0].x, a1 * cs[0].w + b1 * cs[0].z);
+            r1.y = pack2(a2 * cs[1].y + b2 * cs[1].x, a3 * cs[1].w + b3 * cs[1].z);
+          } else {
+            r0.x = turn(r0.x, cs[0].x, cs[0].y);
+            r0.y = turn(r0.y, cs[0].z, cs[0].w);
+            r1.x = turn(r1.x, cs[1].x, cs[1].y);
+            r1.y = turn(r1.y, cs[1].z, cs[1].w);
+          }
+        }
+        if constexpr (HALVES) {
+          *reinterpret_cast<uint2*>(p + c0) = r0;
+          *reinterpret_cast<uint2*>(p + c1) = r1;
+        } else {
+          *reinterpret_cast<uint4*>(p + c0) = make_uint4(r0.x, r0.y, r1.x, r1.y);
+        }
+      }
     }
   }
 }
@@ -155,18 +170,16 @@ cudaError_t launch_rope_table(const float* ids, int L, const RopeFreqs& f, float
                     1, ids, L, f, reinterpret_cast<float2*>(cs));
 }
 
-cudaError_t launch_rope(RopeArgs a, bool halves, cudaStream_t stream) {
-  a.turned_units = halves ? a.rot / 16 : a.rot / 8;
-  a.units = halves ? a.rot / 16 + (a.head_dim - a.rot) / 8 : a.head_dim / 8;
-  const int slots = 256 / a.units;
-  // As few passes over the heads as the slots allow, each of them full.
-  const int passes = (a.heads + slots - 1) / slots;
-  a.heads_par = (a.heads + passes - 1) / passes;
-  a.rows_par = slots / a.heads_par;
-  const long long grid = (a.rows + a.rows_par - 1) / a.rows_par;
-  const unsigned threads = unsigned((a.units * a.heads_par * a.rows_par + 31) / 32 * 32);
-  return halves ? launch_pdl(rope_kernel<true>, dim3(unsigned(grid)), dim3(threads), 0, stream, 1, a)
-                : launch_pdl(rope_kernel<false>, dim3(unsigned(grid)), dim3(threads), 0, stream, 1, a);
+cudaError_t launch_rope(const RopeArgs& a, bool halves, cudaStream_t stream) {
+  int count = 0, heads = 1;
+  for (int i = 0; i < kRopeTensors; ++i)
+    if (a.t[i].heads > 0) count = i + 1, heads = max(heads, a.t[i].heads);
+  // About 256 threads: a batch of heads for each, then further token rows.
+  const int units = a.head_dim / 8, slots = 256 / units;
+  const int ny = min(slots, (heads + kBatch - 1) / kBatch), nz = min(slots / ny, 64);
+  const dim3 grid(unsigned((a.rows + nz - 1) / nz), unsigned(count)), block(units, ny, nz);
+  return halves ? launch_pdl(rope_kernel<true>, grid, block, 0, stream, 1, a)
+                : launch_pdl(rope_kernel<false>, grid, block, 0, stream, 1, a);
 }
 
 }  // namespace tern

@@ -1038,6 +1038,7 @@ tern_status tern_rope(const tern_rope_tensor* tensors, int count, int64_t B, int
   if (B > INT32_MAX || L > INT32_MAX || (B && L > INT32_MAX / B))
     return fail(TERN_ERR_UNSUPPORTED_SHAPE, "rope: B * L above 2^31 - 1");
   RopeArgs a{};
+  int64_t heads = 0;
   Heads x[kRopeTensors], y[kRopeTensors];
   for (int i = 0; i < count; ++i) {
     const tern_rope_tensor& t = tensors[i];
@@ -1046,9 +1047,9 @@ tern_status tern_rope(const tern_rope_tensor* tensors, int count, int64_t B, int
     x[i] = Heads{t.x, B, L, t.heads, head_dim, t.x_b, t.x_l, t.x_h};
     y[i] = Heads{t.y, B, L, t.heads, head_dim, t.y_b, t.y_l, t.y_h};
     a.t[i] = RopeTensor{u16(t.x), u16w(t.y), t.x_b, t.x_l, t.x_h, t.y_b, t.y_l, t.y_h, int(t.heads)};
-    a.heads += int(t.heads);
+    heads += t.heads;
   }
-  if (B == 0 || L == 0 || a.heads == 0) return TERN_OK;
+  if (B == 0 || L == 0 || heads == 0) return TERN_OK;
   if (!cs) return fail(TERN_ERR_INVALID_ARG, "null cs");
   if (!aligned(cs, 16)) return fail(TERN_ERR_MISALIGNED, "cs needs 16-byte alignment");
   if (cs_rows != L && cs_rows != B * L)
@@ -1073,8 +1074,8 @@ tern_status tern_rope(const tern_rope_tensor* tensors, int count, int64_t B, int
     }
   }
   a.cs = cs;
-  a.rows = B * L;
-  a.L = L;
+  a.rows = int(B * L);
+  a.L = int(L);
   a.head_dim = int(head_dim);
   a.rot = int(2 * P);
   a.cs_per_batch = cs_rows != L;
