@@ -184,7 +184,7 @@ struct ResNormArgs {
   int K, post, pre, gate_tanh;
   float post_eps, pre_eps, residual_scale;
 };
-cudaError_t launch_gated_residual_norm(const ResNormArgs& a, cudaStream_t stream);
+cudaError_t launch_gated_residual_norm(const ResNormArgs& a, int sms, cudaStream_t stream);
 
 // Attention of q [B, Lq, H, D] to k, v [B, Lk, Hkv, D] (strides in elements).
 constexpr int kAttnMaxD = 128;

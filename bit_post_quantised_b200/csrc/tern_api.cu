@@ -1220,14 +1220,14 @@ tern_status tern_gated_residual_norm(const tern_gated_residual_norm_args* args, 
   a.gate = u16(t.gate), a.scale = u16(t.scale), a.shift = u16(t.shift);
   a.post_weight = u16(t.post_weight), a.pre_weight = u16(t.pre_weight);
   a.M = t.M, a.ld_x = t.ld_x, a.ld_o = t.ld_o, a.ld_xo = t.ld_x_out, a.ld_h = t.ld_h, a.mod_ld = mod ? t.mod_ld : 0;
-  a.tokens_per_row = t.tokens_per_row;
+  a.tokens_per_row = std::min(t.tokens_per_row, t.M);
   a.K = int(t.K), a.post = t.post_norm, a.pre = t.pre_norm, a.gate_tanh = t.gate_tanh != 0;
   a.post_eps = t.post_eps, a.pre_eps = t.pre_eps, a.residual_scale = t.residual_scale;
   int dev;
   DeviceState* ds;
   tern_status s;
   if ((s = current_device(&dev, &ds)) != TERN_OK) return s;
-  cudaError_t e = launch_gated_residual_norm(a, reinterpret_cast<cudaStream_t>(stream));
+  cudaError_t e = launch_gated_residual_norm(a, ds->sms, reinterpret_cast<cudaStream_t>(stream));
   if (e != cudaSuccess) return cuda_fail(e, "gated_residual_norm launch");
   return TERN_OK;
 }
