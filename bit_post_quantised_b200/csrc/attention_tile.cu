@@ -3,9 +3,12 @@
 //
 //   o[r] = sum_j p_j v[j] / sum_j p_j,   p_j = 2^(scale log2(e) (q[r].k[j] - m)),
 //
-// one pass over the keys with a running reference m and sum.  A CTA owns two
-// 128-row query tiles of one head, both resident in shared memory, and
-// streams K and V tiles (TMA, 128-byte swizzle) through one ring.  Per key
+// one pass over the keys with a running reference m and sum.  A unit is two
+// 128-row query tiles of one head, both resident in shared memory; their K and
+// V tiles stream through one ring (TMA, 128-byte swizzle).  CTAs are
+// persistent, one per SM, and every role runs ahead into its next unit: with
+// few keys the loads and the output of one unit hide behind the products of
+// another (4096 x 512 x 24 heads: 45 us as one CTA per unit).  Per key
 // tile and query tile: S = Q K^T into 128 TMEM columns; four softmax warps
 // read S (a thread owns a row), write P as bf16 over the first half of S;
 // O += P V with P from TMEM and V as stored (rows of keys: the MN-major form of
@@ -24,6 +27,19 @@
 // most) because the tensor core takes both operands in one 16-bit type; the
 // sum is of the unrounded values.
 //
+// What bounds it: for two query tiles and one key tile of 128 channels the
+// tensor core needs 2048 cycles and their 32,768 exponentials, at 16 a cycle,
+// as many.  Measured, a query tile's chain is its softmax (scores 100, maximum
+// 300, exponentials 1450 of at least 1024, barriers) and then the product and
+// the next scores (1024 and their latencies): a period of 3340 cycles, with
+// the two query tiles half a period apart, 0.73 of the measured cuBLAS rate on
+// 4608 x 4608 x 24 heads (210 us).  Tried and slower: part of the exponentials
+// as polynomials on the FMA pipe (the softmax is bound by its dependent
+// issue, not by the exponentials' pipe alone: +3 to +9%), 64-key steps with two
+// score buffers a query tile (scores of 64 keys read Q from shared memory at
+// half the rate the tensor core needs: +4 to +18%), an issuing warp per query
+// tile (the softmaxes fall into step: +29%; in turns: -1.5%, others +3%).
+//
 // Masked keys: S is replaced by -inf there (whatever it holds) and their V
 // rows are overwritten with zeros in shared memory, since 0 * NaN would reach
 // O.  Key tiles past kv_len are not loaded.  A row without a valid key gives
@@ -37,7 +53,8 @@ namespace tern {
 namespace {
 
 constexpr int kBM = 128;        // query rows per tile, two tiles a CTA
-constexpr int kBN = 128;        // keys per tile
+constexpr int kBN = 128;        // keys per K or V tile in shared memory
+constexpr int kFirst = 96;      // keys of a tile whose P is handed over first
 constexpr int kPanel = 16384;   // 128 rows x 64 channels of bf16
 constexpr int kThreads = 384;
 constexpr int kSoftmaxRegs = 208, kOtherRegs = 80;
@@ -102,6 +119,18 @@ __device__ __forceinline__ void mma_ts_4(uint32_t d, uint32_t a, uint64_t b, uin
       : "memory");
 }
 
+// The same for two k16 steps.
+__device__ __forceinline__ void mma_ts_2(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+  asm volatile(
+      "{\n\t.reg .pred p, q, t;\n\t.reg .b32 a1;\n\t.reg .b64 b1;\n\t"
+      "elect.sync _|p, 0xffffffff;\n\tsetp.ne.b32 q, %4, 0;\n\tsetp.eq.b32 t, 0, 0;\n\t"
+      "add.u32 a1, %1, 8;\n\tadd.s64 b1, %2, 128;\n\t"
+      "@p tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, q;\n\t"
+      "@p tcgen05.mma.cta_group::1.kind::f16 [%0], [a1], b1, %3, t;\n\t}" ::"r"(d),
+      "r"(a), "l"(b), "r"(idesc), "r"(acc)
+      : "memory");
+}
+
 __device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap* map, int32_t c0, int32_t c1, int32_t c2,
                                             int32_t c3, uint32_t bar) {
   asm volatile(
@@ -122,17 +151,66 @@ __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
   return d;
 }
 
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float d;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
+
+// Waits like mbar_wait, in little code: the issuers' and the softmax warps'
+// loops are long enough to be bound by instruction fetches where every wait
+// carries its polling loop.
+__device__ __forceinline__ bool bar_wait(uint32_t bar, uint32_t parity, uint64_t limit_ns, unsigned int* status) {
+  if (mbar_try_wait(bar, parity)) return true;
+  const long long t0 = clock64(), limit = (long long)(limit_ns * 2ull);
+#pragma unroll 1
+  while (!mbar_try_wait(bar, parity)) {
+    if (clock64() - t0 > limit) {
+      atomicOr(status, kStatusTimeout);
+      return false;
+    }
+  }
+  return true;
+}
+
+// u / d for the u < 2^31 that the reciprocal was made for (see div_by in internal.h).
+__device__ __forceinline__ int div_of(int u, const DivBy& d) { return d.mul ? int(__umulhi(unsigned(u), d.mul) >> d.shift) : u; }
+
+// One work unit: two query tiles of a head.
+struct Unit {
+  int b, h, hk, q0;
+  int nq;   // query tiles with a row
+  int len;  // keys before kv_len
+  int n;    // key tiles
+};
+template <bool MASK>
+__device__ __forceinline__ Unit unit_of(const AttnTileArgs& t, int u) {
+  const AttnArgs& a = t.a;
+  Unit x;
+  const int bh = div_of(u, t.by_pairs);
+  x.b = div_of(bh, t.by_heads);
+  x.h = bh - x.b * a.H;
+  x.hk = div_of(x.h, t.by_group);
+  x.q0 = (u - bh * t.pairs) * 2 * kBM;
+  x.nq = x.q0 + kBM < a.Lq ? 2 : 1;
+  x.len = MASK && a.kv_len ? max(0, min(a.Lk, a.kv_len[x.b])) : a.Lk;
+  x.n = (x.len + kBN - 1) / kBN;
+  return x;
+}
+
 template <int DP, bool MASK>
 __global__ void __launch_bounds__(kThreads, 1) attention_tile_kernel(const __grid_constant__ AttnTileArgs t) {
   using C = TileShape<DP>;
   constexpr int S = C::kStages;
   constexpr int kMaskSlots = 4;
   __shared__ __align__(8) uint64_t q_full[2];      // a query tile has landed
+  __shared__ __align__(8) uint64_t q_empty[2];     // the unit's last scores are done
   __shared__ __align__(8) uint64_t kv_full[S];     // ring slot landed
   __shared__ __align__(8) uint64_t kv_empty[S];    // every product reading the slot is done
   __shared__ __align__(8) uint64_t s_full[2];      // S of the next key tile is in TMEM
-  __shared__ __align__(8) uint64_t p_full[2];      // P is in TMEM (and O rescaled)
-  __shared__ __align__(8) uint64_t o_done[2];      // O += P V is done
+  __shared__ __align__(8) uint64_t p_full[2][2];   // P of the first keys is there (and O rescaled); of the rest
+  __shared__ __align__(8) uint64_t o_done[2];      // the unit's O is complete
+  __shared__ __align__(8) uint64_t o_free[2];      // the unit's O has been read
   __shared__ __align__(8) uint64_t drain_bar;      // every MMA issued is done
   __shared__ __align__(8) uint64_t v_ready[MASK ? kMaskSlots : 1];   // masked rows of a tile's V are zero
   __shared__ __align__(8) uint64_t m_full[MASK ? kMaskSlots : 1];    // validity of a key tile written
@@ -147,20 +225,17 @@ __global__ void __launch_bounds__(kThreads, 1) attention_tile_kernel(const __gri
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t smem_base = (smem_u32(dyn_smem) + 1023u) & ~1023u;
   const uint32_t ring = smem_base + 2 * C::kTile;
-
-  const int pair = int(blockIdx.x % unsigned(t.pairs));
-  const int bh = int(blockIdx.x / unsigned(t.pairs));
-  const int h = bh % a.H, b = bh / a.H;
-  const int hk = h / (a.H / a.Hkv);
-  const int q0 = pair * 2 * kBM;
-  const int nq = q0 + kBM < a.Lq ? 2 : 1;  // query tiles with a row
+  const int units = t.units, u0 = int(blockIdx.x), ustep = int(gridDim.x);
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < 2; ++i) {
       mbar_init(smem_u32(&q_full[i]), 1);
+      mbar_init(smem_u32(&q_empty[i]), 1);
       mbar_init(smem_u32(&s_full[i]), 1);
-      mbar_init(smem_u32(&p_full[i]), 4);
+      mbar_init(smem_u32(&p_full[i][0]), 4);
+      mbar_init(smem_u32(&p_full[i][1]), 4);
       mbar_init(smem_u32(&o_done[i]), 1);
+      mbar_init(smem_u32(&o_free[i]), 4);
     }
     for (int s = 0; s < S; ++s) {
       mbar_init(smem_u32(&kv_full[s]), 1);
@@ -170,7 +245,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_tile_kernel(const __gri
       for (int s = 0; s < kMaskSlots; ++s) {
         mbar_init(smem_u32(&m_full[s]), 1);
         mbar_init(smem_u32(&v_ready[s]), 1);
-        mbar_init(smem_u32(&m_empty[s]), 4 * nq);
+        mbar_init(smem_u32(&m_empty[s]), 8);
       }
     mbar_init(smem_u32(&drain_bar), 1);
     fence_barrier_init();
@@ -186,131 +261,152 @@ __global__ void __launch_bounds__(kThreads, 1) attention_tile_kernel(const __gri
   pdl_trigger();
   tc_fence_after();
   const uint32_t tmem = tmem_base_sh;
-  const int len = MASK && a.kv_len ? max(0, min(a.Lk, a.kv_len[b])) : a.Lk;
-  const int n = (len + kBN - 1) / kBN;  // key tiles
 
   if (warp < 8) {
     // ------------------------------------------------------ softmax, output
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs));
     const int i = warp >> 2;  // query tile
-    const int row = q0 + i * kBM + (warp & 3) * 32 + lane;
     const uint32_t lane_off = uint32_t((warp & 3) * 32) << 16;
     const uint32_t ts = tmem + lane_off + i * kBN, to = tmem + lane_off + 256 + i * DP;
     const float sl = a.scale_log2;
-    float m = -INFINITY, sum = 0.f;
+    const float2 sl2 = make_float2(sl, sl);
+    uint32_t sp = 0, op = 0;  // phases of s_full and o_done
+    int mt = 0;  // key tiles so far (the slot and phase of the validity words)
     bool ok = true;
-    if (i < nq) {
-      for (int j = 0; j < n; ++j) {
-        uint32_t w[4] = {~0u, ~0u, ~0u, ~0u};  // validity of the tile's keys
-        if constexpr (MASK) {
-          const int ms = j % kMaskSlots;
-          ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(&m_full[ms]), (j / kMaskSlots) & 1, lim, st));
-          if (!ok) break;
-          const uint4 mw = *reinterpret_cast<const uint4*>(m_words[ms]);
-          w[0] = mw.x, w[1] = mw.y, w[2] = mw.z, w[3] = mw.w;
-          __syncwarp();
-          if (lane == 0) mbar_arrive(smem_u32(&m_empty[ms]));
-        } else if (len - j * kBN < kBN) {
-          const int rem = len - j * kBN;
-#pragma unroll
-          for (int c = 0; c < 4; ++c) w[c] = rem >= 32 * c + 32 ? ~0u : rem <= 32 * c ? 0u : (1u << (rem - 32 * c)) - 1u;
+    for (int u = u0; u < units && ok; u += ustep) {
+      const Unit x = unit_of<MASK>(t, u);
+      if (i >= x.nq) {
+        if constexpr (MASK) {  // not this warp's keys, but its turn in the slots
+          for (int j = 0; j < x.n && ok; ++j, ++mt) {
+            const int ms = mt % kMaskSlots;
+            ok = __all_sync(0xffffffffu, bar_wait(smem_u32(&m_full[ms]), (mt / kMaskSlots) & 1, lim, st));
+            if (lane == 0) mbar_arrive(smem_u32(&m_empty[ms]));
+          }
         }
-        ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(&s_full[i]), j & 1, lim, st));
+        continue;
+      }
+      float m = -INFINITY, sum = 0.f;
+      for (int j = 0; j < x.n; ++j) {
+        ok = __all_sync(0xffffffffu, bar_wait(smem_u32(&s_full[i]), sp, lim, st));
         if (!ok) break;
+        sp ^= 1;
         tc_fence_after();
         uint32_t v[4][32];
 #pragma unroll
         for (int c = 0; c < 4; ++c) tmem_ld32(ts + 32 * c, v[c]);
         tmem_wait_ld();
-        if ((w[0] & w[1] & w[2] & w[3]) != ~0u) {
+        if (MASK || x.len - j * kBN < kBN) {
+          uint32_t w[4];  // validity of the tile's keys
+          if constexpr (MASK) {
+            const int ms = mt % kMaskSlots;
+            ok = __all_sync(0xffffffffu, bar_wait(smem_u32(&m_full[ms]), (mt / kMaskSlots) & 1, lim, st));
+            if (!ok) break;
+            const uint4 mw = *reinterpret_cast<const uint4*>(m_words[ms]);
+            w[0] = mw.x, w[1] = mw.y, w[2] = mw.z, w[3] = mw.w;
+            __syncwarp();
+            if (lane == 0) mbar_arrive(smem_u32(&m_empty[ms]));
+            ++mt;
+          } else {
+            const int rem = x.len - j * kBN;
 #pragma unroll
-          for (int c = 0; c < 4; ++c)
+            for (int c = 0; c < 4; ++c) w[c] = rem >= 32 * c + 32 ? ~0u : rem <= 32 * c ? 0u : (1u << (rem - 32 * c)) - 1u;
+          }
+          if (!MASK || (w[0] & w[1] & w[2] & w[3]) != ~0u) {
 #pragma unroll
-            for (int e = 0; e < 32; ++e)
-              if (!((w[c] >> e) & 1u)) v[c][e] = 0xFF800000u;  // -inf
+            for (int c = 0; c < 4; ++c)
+#pragma unroll
+              for (int e = 0; e < 32; ++e)
+                if (!((w[c] >> e) & 1u)) v[c][e] = 0xFF800000u;  // -inf
+          }
         }
         float top[4];
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
-          top[c] = __uint_as_float(v[c][0]);
+          top[c] = fmaxf(__uint_as_float(v[c][0]), __uint_as_float(v[c][1]));
 #pragma unroll
-          for (int e = 1; e < 32; ++e) top[c] = fmaxf(top[c], __uint_as_float(v[c][e]));
+          for (int e = 2; e < 32; e += 2) top[c] = max3(top[c], __uint_as_float(v[c][e]), __uint_as_float(v[c][e + 1]));
         }
-        const float to_max = fmaxf(fmaxf(m, fmaxf(top[0], top[1])), fmaxf(top[2], top[3]));
-        const bool move = (to_max - m) * sl > 8.f;  // false for NaN: both still -inf
+        const float to_max = fmaxf(max3(m, top[0], top[1]), fmaxf(top[2], top[3]));
+        const bool move = (to_max - m) * sl > 8.f;  // false for NaN: both still -inf, or a NaN score
         if (__any_sync(0xffffffffu, move)) {
           const float f = move ? exp2_fast((m - to_max) * sl) : 1.f;
           if (move) m = to_max;
           sum *= f;
           if (j > 0) {
-            ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(&o_done[i]), (j - 1) & 1, lim, st));
-            if (!ok) break;
-            tc_fence_after();
+            // These scores were issued behind the last product: that one is done.
 #pragma unroll 1
             for (int c = 0; c < DP; c += 32) {
-              uint32_t x[32];
-              tmem_ld32(to + c, x);
+              uint32_t y[32];
+              tmem_ld32(to + c, y);
               tmem_wait_ld();
 #pragma unroll
-              for (int e = 0; e < 32; ++e) x[e] = __float_as_uint(__uint_as_float(x[e]) * f);
-              tmem_st32(to + c, x);
+              for (int e = 0; e < 32; ++e) y[e] = __float_as_uint(__uint_as_float(y[e]) * f);
+              tmem_st32(to + c, y);
             }
           }
         }
         const float base = m == -INFINITY ? 0.f : -m * sl;
-        const float2 sl2 = make_float2(sl, sl), base2 = make_float2(base, base);
+        const float2 base2 = make_float2(base, base);
         float2 acc[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
           uint32_t p[16];
 #pragma unroll
           for (int e = 0; e < 16; ++e) {
-            float2 x = fma2(make_float2(__uint_as_float(v[c][2 * e]), __uint_as_float(v[c][2 * e + 1])), sl2, base2);
-            x.x = exp2_fast(x.x);
-            x.y = exp2_fast(x.y);
-            acc[e & 1] = add2(acc[e & 1], x);
-            p[e] = pack2(x.x, x.y);
+            float2 y = fma2(make_float2(__uint_as_float(v[c][2 * e]), __uint_as_float(v[c][2 * e + 1])), sl2, base2);
+            y.x = exp2_fast(y.x);
+            y.y = exp2_fast(y.y);
+            acc[e & 1] = add2(acc[e & 1], y);
+            p[e] = pack2(y.x, y.y);
           }
-          tmem_st16(ts + 16 * c, p);
+          tmem_st16(ts + 16 * c, p);  // P over the first 64 columns of S
+          if (32 * c + 32 == kFirst || c == 3) {
+            tmem_wait_st();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(smem_u32(&p_full[i][c == 3]));
+          }
         }
-        tmem_wait_st();
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(smem_u32(&p_full[i]));
         acc[0] = add2(acc[0], acc[1]);
         sum += acc[0].x + acc[0].y;
       }
-      if (ok && n > 0) {
-        ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(&o_done[i]), (n - 1) & 1, lim, st));
+      if (!ok) break;
+      if (x.n > 0) {
+        ok = __all_sync(0xffffffffu, bar_wait(smem_u32(&o_done[i]), op, lim, st));
+        if (!ok) break;
+        op ^= 1;
         tc_fence_after();
       }
-      if (ok) {
-        const float inv = sum == 0.f ? 0.f : 1.f / sum;
-        uint16_t* op = a.o + b * a.o_b + (long long)row * a.o_l + h * a.o_h;
+      const int row = x.q0 + i * kBM + (warp & 3) * 32 + lane;
+      const float inv = sum == 0.f ? 0.f : 1.f / sum;
+      uint16_t* op = a.o + x.b * a.o_b + (long long)row * a.o_l + x.h * a.o_h;
 #pragma unroll 1
-        for (int c = 0; c < DP; c += 32) {
-          uint32_t x[32];
-          if (n > 0) {
-            tmem_ld32(to + c, x);
-            tmem_wait_ld();
-          } else {
+      for (int c = 0; c < DP; c += 32) {
+        uint32_t y[32];
+        if (x.n > 0) {
+          tmem_ld32(to + c, y);
+          tmem_wait_ld();
+        } else {
 #pragma unroll
-            for (int e = 0; e < 32; ++e) x[e] = 0u;
-          }
-          if (row < a.Lq) {
+          for (int e = 0; e < 32; ++e) y[e] = 0u;
+        }
+        if (x.n > 0 && c + 32 == DP) {
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(smem_u32(&o_free[i]));
+        }
+        if (row < a.Lq) {
 #pragma unroll
-            for (int e = 0; e < 32; e += 8) {
-              if (c + e < a.D) {
-                uint32_t y[4];
+          for (int e = 0; e < 32; e += 8) {
+            if (c + e < a.D) {
+              uint32_t z[4];
 #pragma unroll
-                for (int u = 0; u < 4; ++u)
-                  y[u] = pack2(__uint_as_float(x[e + 2 * u]) * inv, __uint_as_float(x[e + 2 * u + 1]) * inv);
-                *reinterpret_cast<uint4*>(op + c + e) = make_uint4(y[0], y[1], y[2], y[3]);
-              }
+              for (int k = 0; k < 4; ++k)
+                z[k] = pack2(__uint_as_float(y[e + 2 * k]) * inv, __uint_as_float(y[e + 2 * k + 1]) * inv);
+              *reinterpret_cast<uint4*>(op + c + e) = make_uint4(z[0], z[1], z[2], z[3]);
             }
           }
         }
-        tc_fence_before();
       }
     }
   } else {
@@ -318,55 +414,102 @@ __global__ void __launch_bounds__(kThreads, 1) attention_tile_kernel(const __gri
     if (warp == 8) {
       // ---------------------------------------------------- MMA issuer
       const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
-      bool ok = n > 0;
+      bool ok = true;
       auto wait = [&](uint64_t* bar, int parity) {
-        return __shfl_sync(0xffffffffu, mbar_wait(smem_u32(bar), parity, lim, st), 0);
+        return bool(__all_sync(0xffffffffu, bar_wait(smem_u32(bar), parity, lim, st)));
       };
-      auto scores = [&](int i, int slot) {
-        const uint64_t qd = sw128_kmajor_desc(smem_base + i * C::kTile), kd = sw128_kmajor_desc(ring + slot * C::kTile);
-        mma_ss_panel(tm + i * kBN, qd, kd, C::kIdescS, 0);
-        if constexpr (C::kPanels == 2)
-          mma_ss_panel(tm + i * kBN, qd + (kPanel >> 4), kd + (kPanel >> 4), C::kIdescS, 1);
-        mma_commit_elected(smem_u32(&s_full[i]));
+      // Key tiles in order, over all units; for each query tile in turn its
+      // product, as its P comes in two parts, and right behind it the scores
+      // of the next key tile (of the next unit, too) into the same S: MMAs of
+      // one thread run in order.  Taking the query tiles in turn also keeps
+      // their softmaxes half a period apart, one with the other's products
+      // (with an issuer each they fell into step, and joint attention of
+      // 4608 tokens took 271 us instead of 217).
+      const uint64_t qd0 = sw128_kmajor_desc(smem_base);
+      const uint64_t kd0 = sw128_kmajor_desc(ring), vd0 = sw128_mnmajor_desc(ring);
+      constexpr uint32_t kSlot = C::kTile >> 4;  // in descriptor units
+      auto next_unit = [&](int u, Unit& x) {  // the first unit from u on with keys
+        for (; u < units; u += ustep) {
+          x = unit_of<MASK>(t, u);
+          if (x.n > 0) break;
+        }
+        return u;
       };
-      for (int i = 0; i < nq && ok; ++i) {
-        ok = wait(&q_full[i], 0) && (i > 0 || wait(&kv_full[0], 0));
-        if (!ok) break;
-        tc_fence_after();
-        scores(i, 0);
-      }
-      if (ok) mma_commit_elected(smem_u32(&kv_empty[0]));
-      for (int j = 0; j < n && ok; ++j) {
-        const int it = 2 * j + 1, vs = it % S;                // V of tile j
-        const int kt = it + 1, ks = kt % S;                   // K of tile j + 1
-        ok = wait(&kv_full[vs], (it / S) & 1) && (!MASK || wait(&v_ready[j % kMaskSlots], (j / kMaskSlots) & 1));
-        for (int i = 0; i < nq && ok; ++i) {
-          ok = wait(&p_full[i], j & 1);
-          if (!ok) break;
-          tc_fence_after();
-          const uint64_t vd = sw128_mnmajor_desc(ring + vs * C::kTile);
-          mma_ts_4(tm + 256 + i * DP, tm + i * kBN, vd, C::kIdescO, j > 0);
-          mma_ts_4(tm + 256 + i * DP, tm + i * kBN + 32, vd + 512, C::kIdescO, 1);
-          mma_commit_elected(smem_u32(&o_done[i]));
-          if (i == nq - 1) mma_commit_elected(smem_u32(&kv_empty[vs]));
-          if (j + 1 < n) {
-            // S of the next tile overwrites this P: MMAs of one thread run in order.
-            if (i == 0) ok = wait(&kv_full[ks], (kt / S) & 1);
-            if (!ok) break;
-            tc_fence_after();
-            scores(i, ks);
-            if (i == nq - 1) mma_commit_elected(smem_u32(&kv_empty[ks]));
+      Unit y{};  // the unit of the tile whose scores are next
+      int un = next_unit(u0, y), yj = 0;
+      bool more = un < units, last = false;  // last: the tile whose product is next is its unit's last
+      int nq = 0, j = 0, tile = 0;           // its query tiles (0: none yet), its place in the unit and among all
+      int ks = 0, vs = 1 % S;
+      uint32_t kp = 0, vp = 0;               // phases of the ring
+      uint32_t pp = 0, qp = 0, op = 3;       // bit i: of p_full, q_full, o_free
+      while (ok && (more || nq > 0)) {
+        const int nq_next = more ? y.nq : 0;
+        const bool last_next = yj == y.n - 1;
+        if (nq > 0) {
+          ok = wait(&kv_full[vs], vp);
+          if (MASK && ok) ok = wait(&v_ready[tile % kMaskSlots], (tile / kMaskSlots) & 1);
+        }
+        if (ok && more) ok = wait(&kv_full[ks], kp);
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const uint32_t ts = tm + i * kBN, to = tm + 256 + i * DP;
+          if (ok && i < nq) {
+            if (j == 0) {
+              ok = wait(&o_free[i], (op >> i) & 1);
+              op ^= 1u << i;
+            }
+            const uint64_t vd = vd0 + uint32_t(vs) * kSlot;
+            if (ok) ok = wait(&p_full[i][0], (pp >> i) & 1);
+            if (ok) {
+              tc_fence_after();
+              mma_ts_4(to, ts, vd, C::kIdescO, j > 0);
+              mma_ts_2(to, ts + 32, vd + 512, C::kIdescO, 1);
+              ok = wait(&p_full[i][1], (pp >> i) & 1);
+            }
+            pp ^= 1u << i;
+            if (ok) {
+              tc_fence_after();
+              mma_ts_2(to, ts + 48, vd + 768, C::kIdescO, 1);
+              if (last) mma_commit_elected(smem_u32(&o_done[i]));
+              if (i == nq - 1) mma_commit_elected(smem_u32(&kv_empty[vs]));
+            }
+          }
+          if (ok && i < nq_next) {
+            if (yj == 0) {
+              ok = wait(&q_full[i], (qp >> i) & 1);
+              qp ^= 1u << i;
+            }
+            if (ok) {
+              tc_fence_after();
+              const uint64_t qd = qd0 + uint32_t(i) * kSlot, kd = kd0 + uint32_t(ks) * kSlot;
+              mma_ss_panel(ts, qd, kd, C::kIdescS, 0);
+              if constexpr (C::kPanels == 2) mma_ss_panel(ts, qd + (kPanel >> 4), kd + (kPanel >> 4), C::kIdescS, 1);
+              mma_commit_elected(smem_u32(&s_full[i]));
+              if (last_next) mma_commit_elected(smem_u32(&q_empty[i]));
+              if (i == nq_next - 1) mma_commit_elected(smem_u32(&kv_empty[ks]));
+            }
+          }
+        }
+        if (nq > 0) {
+          vs += 2, vp ^= uint32_t(vs >= S), vs -= vs >= S ? S : 0;
+          ++tile;
+        }
+        nq = nq_next, j = yj, last = last_next;
+        if (more) {
+          ks += 2, kp ^= uint32_t(ks >= S), ks -= ks >= S ? S : 0;
+          if (++yj == y.n) {
+            yj = 0;
+            un = next_unit(un + ustep, y);
+            more = un < units;
           }
         }
       }
-      if (n > 0) {
-        mma_commit_elected(smem_u32(&drain_bar));
-        __syncwarp();
-        mbar_wait(smem_u32(&drain_bar), 0, lim, st);
-      }
+      mma_commit_elected(smem_u32(&drain_bar));
+      __syncwarp();
+      mbar_wait(smem_u32(&drain_bar), 0, lim, st);
     } else if (warp == 9) {
       // ---------------------------------------------------- TMA
-      if (lane == 0 && n > 0) {
+      if (lane == 0) {
         prefetch_tensormap(&t.tq);
         prefetch_tensormap(&t.tk);
         prefetch_tensormap(&t.tv);
@@ -375,63 +518,86 @@ __global__ void __launch_bounds__(kThreads, 1) attention_tile_kernel(const __gri
 #pragma unroll
           for (int p = 0; p < C::kPanels; ++p) tma_load_4d(dst + p * kPanel, map, 64 * p, r, hh, bb, smem_u32(bar));
         };
-        load(smem_base, &t.tq, q0, h * t.q_h, b * t.q_b, &q_full[0]);
-        int it = 0;
+        int it = 0, qc[2] = {0, 0};
         bool ok = true;
-        for (; it < 2 * n; ++it) {
-          const int s = it % S;
-          ok = mbar_wait(smem_u32(&kv_empty[s]), ((it / S) & 1) ^ 1, lim, st);
-          if (!ok) break;
-          if (it & 1)
-            load(ring + s * C::kTile, &t.tv, (it >> 1) * kBN, hk * t.v_h, b * t.v_b, &kv_full[s]);
-          else
-            load(ring + s * C::kTile, &t.tk, (it >> 1) * kBN, hk * t.k_h, b * t.k_b, &kv_full[s]);
-          if (it == 0 && nq > 1) load(smem_base + C::kTile, &t.tq, q0 + kBM, h * t.q_h, b * t.q_b, &q_full[1]);
+        for (int u = u0; u < units && ok; u += ustep) {
+          const Unit x = unit_of<MASK>(t, u);
+          for (int k = 0; k < 2 * x.n && ok; ++k) {
+            const int s = it % S;
+            ok = mbar_wait(smem_u32(&kv_empty[s]), ((it / S) & 1) ^ 1, lim, st);
+            if (!ok) break;
+            if (k & 1)
+              load(ring + s * C::kTile, &t.tv, (k >> 1) * kBN, x.hk * t.v_h, x.b * t.v_b, &kv_full[s]);
+            else
+              load(ring + s * C::kTile, &t.tk, (k >> 1) * kBN, x.hk * t.k_h, x.b * t.k_b, &kv_full[s]);
+            ++it;
+            if (k == 0) {
+#pragma unroll
+              for (int i = 0; i < 2; ++i) {
+                if (i >= x.nq || !ok) break;
+                ok = mbar_wait(smem_u32(&q_empty[i]), (qc[i] & 1) ^ 1, lim, st);
+                if (!ok) break;
+                load(smem_base + i * C::kTile, &t.tq, x.q0 + i * kBM, x.h * t.q_h, x.b * t.q_b, &q_full[i]);
+                ++qc[i];
+              }
+            }
+          }
         }
         // No copy may still be landing when the CTA exits.
-        for (int i = 0; i < nq && (i == 0 || it > 0); ++i) mbar_wait(smem_u32(&q_full[i]), 0, lim, st);
-        for (int x = it > S ? it - S : 0; x < it; ++x) mbar_wait(smem_u32(&kv_full[x % S]), (x / S) & 1, lim, st);
+        for (int i = 0; i < 2; ++i)
+          if (qc[i] > 0) mbar_wait(smem_u32(&q_full[i]), (qc[i] - 1) & 1, lim, st);
+        for (int k = it > S ? it - S : 0; k < it; ++k) mbar_wait(smem_u32(&kv_full[k % S]), (k / S) & 1, lim, st);
       }
       __syncwarp();
     } else if (MASK && warp == 10) {
       // ---------------------------------------------------- key validity
-      const uint8_t* mask = a.key_mask ? a.key_mask + b * a.mask_ld : nullptr;
-      for (int j = 0; j < n; ++j) {
-        const int ms = j % kMaskSlots, it = 2 * j + 1, vs = it % S;
-        uint32_t w[4];
+      int mt = 0;
+      bool ok = true;
+      for (int u = u0; u < units && ok; u += ustep) {
+        const Unit x = unit_of<MASK>(t, u);
+        const uint8_t* mask = a.key_mask ? a.key_mask + x.b * a.mask_ld : nullptr;
+        for (int j = 0; j < x.n && ok; ++j, ++mt) {
+          const int ms = mt % kMaskSlots, it = 2 * mt + 1, vs = it % S;
+          uint32_t w[4];
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          const int key = j * kBN + 32 * c + lane;
-          w[c] = __ballot_sync(0xffffffffu, key < len && (!mask || mask[key]));
+          for (int c = 0; c < 4; ++c) {
+            const int key = j * kBN + 32 * c + lane;
+            w[c] = __ballot_sync(0xffffffffu, key < x.len && (!mask || mask[key]));
+          }
+          ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(&m_empty[ms]), ((mt / kMaskSlots) & 1) ^ 1, lim, st));
+          if (!ok) break;
+          if (lane == 0) {
+            *reinterpret_cast<uint4*>(m_words[ms]) = make_uint4(w[0], w[1], w[2], w[3]);
+            mbar_arrive(smem_u32(&m_full[ms]));
+          }
+          // The slot's V has landed before its masked rows are cleared; the
+          // clearing is made visible to the tensor core before the arrival.
+          ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(&kv_full[vs]), (it / S) & 1, lim, st));
+          if (!ok) break;
+          if ((w[0] & w[1] & w[2] & w[3]) != ~0u) {
+#pragma unroll
+            for (int c = 0; c < 4; ++c)
+              if (!((w[c] >> lane) & 1u)) {
+                uint8_t* r = dyn_smem + (ring - smem_u32(dyn_smem)) + vs * C::kTile + (32 * c + lane) * 128;
+#pragma unroll
+                for (int p = 0; p < C::kPanels; ++p)
+#pragma unroll
+                  for (int k = 0; k < 8; ++k) *reinterpret_cast<uint4*>(r + p * kPanel + 16 * k) = make_uint4(0u, 0u, 0u, 0u);
+              }
+            fence_proxy_async_smem();
+          }
+          __syncwarp();
+          if (lane == 0) mbar_arrive(smem_u32(&v_ready[ms]));
         }
-        if (!__all_sync(0xffffffffu, mbar_wait(smem_u32(&m_empty[ms]), ((j / kMaskSlots) & 1) ^ 1, lim, st))) break;
-        if (lane == 0) {
-          *reinterpret_cast<uint4*>(m_words[ms]) = make_uint4(w[0], w[1], w[2], w[3]);
-          mbar_arrive(smem_u32(&m_full[ms]));
-        }
-        // The slot's V has landed before its masked rows are cleared; the
-        // clearing is made visible to the tensor core before the arrival.
-        if (!__all_sync(0xffffffffu, mbar_wait(smem_u32(&kv_full[vs]), (it / S) & 1, lim, st))) break;
-        if ((w[0] & w[1] & w[2] & w[3]) != ~0u) {
-#pragma unroll
-          for (int c = 0; c < 4; ++c)
-            if (!((w[c] >> lane) & 1u)) {
-              uint8_t* r = dyn_smem + (ring - smem_u32(dyn_smem)) + vs * C::kTile + (32 * c + lane) * 128;
-#pragma unroll
-              for (int p = 0; p < C::kPanels; ++p)
-#pragma unroll
-                for (int x = 0; x < 8; ++x) *reinterpret_cast<uint4*>(r + p * kPanel + 16 * x) = make_uint4(0u, 0u, 0u, 0u);
-            }
-          fence_proxy_async_smem();
-        }
-        __syncwarp();
-        if (lane == 0) mbar_arrive(smem_u32(&v_ready[ms]));
       }
     }
   }
   // Every role is done with TMEM and the barriers.
   __syncthreads();
-  if (warp == 8) tmem_dealloc(tmem, 512);
+  if (warp == 8) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
 }
 
 template <int DP, bool MASK>
@@ -452,7 +618,7 @@ cudaError_t launch_one(const AttnTileArgs& t, cudaStream_t stream) {
     if (e != cudaSuccess) return e;
     ready_dev = dev;
   }
-  return launch_pdl(attention_tile_kernel<DP, MASK>, dim3(unsigned(t.pairs) * unsigned(t.a.B * t.a.H)), dim3(kThreads),
+  return launch_pdl(attention_tile_kernel<DP, MASK>, dim3(unsigned(t.units < t.ctas ? t.units : t.ctas)), dim3(kThreads),
                     C::kSmem, stream, 1, t);
 }
 

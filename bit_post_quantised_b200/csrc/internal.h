@@ -199,6 +199,19 @@ struct AttnArgs {
   int B, Lq, Lk, H, Hkv, D;
   float scale_log2;         // softmax scale * log2(e)
 };
+// Division of u < 2^31 by d: u * ceil(2^(31 + l) / d) >> (31 + l), l =
+// ceil(log2 d), is exact since the multiplier is off by less than 2^l / d units;
+// mul = 0 stands for d = 1.
+struct DivBy {
+  unsigned mul, shift;
+};
+inline DivBy div_by(unsigned d) {
+  unsigned l = 0;
+  while (l < 31 && (1u << l) < d) ++l;
+  if (l == 0) return {0u, 0u};
+  const unsigned long long s = 1ull << (31 + l);
+  return {unsigned((s + d - 1) / d), l - 1};
+}
 // The same with the tensor maps {D, L, H, B} (box {64, 128, 1, 1}, 128-byte
 // swizzle) that the tile kernel loads through; q_h ... are 0 for a dimension
 // that the map has once (a broadcast), else 1.
@@ -206,7 +219,10 @@ struct alignas(64) AttnTileArgs {
   CUtensorMap tq, tk, tv;
   AttnArgs a;
   int q_b, q_h, k_b, k_h, v_b, v_h;
-  int pairs;  // of 128-row query tiles
+  int pairs;  // of 128-row query tiles, per head
+  int units;  // pairs * B * H
+  int ctas;   // resident at once
+  DivBy by_pairs, by_heads, by_group;  // pairs, H, H / Hkv
   unsigned long long wait_limit_ns;
   unsigned int* status;
 };

@@ -1152,6 +1152,11 @@ tern_status tern_attention(const tern_attention_args* args, tern_stream_t stream
     const int64_t pairs = (t.Lq + 255) / 256;
     if (pairs * t.B * t.H > INT32_MAX) return fail(TERN_ERR_UNSUPPORTED_SHAPE, "attention: too many query rows");
     ta.pairs = int(pairs);
+    ta.units = int(pairs * t.B * t.H);
+    ta.ctas = ds->sms;
+    ta.by_pairs = div_by(unsigned(pairs));
+    ta.by_heads = div_by(unsigned(t.H));
+    ta.by_group = div_by(unsigned(t.H / t.Hkv));
     ta.wait_limit_ns = g_wait_limit_ns.load();
     ta.status = ds->status;
     e = launch_attention_tile(ta, reinterpret_cast<cudaStream_t>(stream));
