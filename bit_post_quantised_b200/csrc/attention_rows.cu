@@ -7,21 +7,30 @@
 // The G = H / Hkv query heads that share a key-value head are rows of one
 // 16-row tile (row r: query r / G, head r % G of the group), so K and V are
 // read once for all of them; with few rows the bound is that read.  A unit is
-// (batch entry, key-value head, 16 rows); a cluster of S CTAs splits its keys
-// in blocks of 16 dealt round-robin to the S * 4 warps.  A warp keeps its
-// running row maxima, sums and 16 x D output in registers, all fp32, and
-// streams its blocks with 16-byte loads straight into mma.sync fragments:
+// (batch entry, key-value head, 16 rows); a cluster of up to 16 CTAs splits its
+// keys in blocks of 16 dealt round-robin to all its warps.  A warp keeps its
+// running row maxima, sums and 16 x D output in registers, all fp32, and has
+// a ring of its own in shared memory for its next blocks (cp.async, no barrier
+// with other warps; loaded straight into registers, one block ahead, two
+// thirds of the warps' time was the wait for V: 1.5 TB/s on 16,384 keys).
 //   - the order of the products' channels is free as long as q and k agree,
-//     so thread t of a quad takes channels 32 i + 8 t .. + 7 of a key as
-//     two k16 steps' fragments (64 consecutive bytes a quad and key);
+//     so thread t of a quad takes channels 32 i + 8 t .. + 7 of a key, 16
+//     bytes, as two k16 steps' fragments;
 //   - the output channels' places in the n8 tiles are free too: row g of the
-//     quad owns channels 64 c + 8 g .. + 7 of a value row.
-// No shared memory is touched before the join, and the next block's keys are
-// in flight while this one is computed.  The probabilities go to the tensor
-// cores as the sum of two bf16 (value and remainder): the extra product is
-// free under the memory bound and leaves only the final rounding.  Masked
-// keys have their score replaced (not added to) and their value row zeroed,
-// so whatever they hold is not seen; a row without a valid key gives zeros.
+//     quad owns channels 64 c + 8 g .. + 7 of a value row, and keys 2t, 2t + 1
+//     of each eight, the ones whose scores it holds.
+// 16-byte groups are swizzled by the key so that both reads meet every bank.
+// The probabilities go to the tensor cores as the sum of two bf16 (value and
+// remainder): the extra product is free under the memory bound and leaves
+// only the final rounding.  Masked keys have their score replaced (not added
+// to) and their value row zeroed, so whatever they hold is not seen; a row
+// without a valid key gives zeros.
+//
+// The ring is sized for two CTAs an SM, which also lets eight clusters of 16
+// be resident.  Long caches of few heads are bound by the instructions of a
+// block's chain (16,384 keys x 8 heads: 29.8 us, 2.3 TB/s; blocks of 32 keys,
+// one CTA an SM, leave room for seven clusters only: 46 us), short calls by
+// their latency (512 keys x 24 heads, one query: 7.3 us).
 //
 // Join: the four warps of a CTA combine their (max, sum, output) through
 // shared memory, then the CTAs of the cluster through distributed shared
@@ -36,6 +45,7 @@ namespace {
 
 constexpr int kWarps = 4;
 constexpr int kRows = 16;
+constexpr int kKeys = 16;  // of a block
 
 __device__ __forceinline__ void mma_16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                           uint32_t b1) {
@@ -49,6 +59,16 @@ __device__ __forceinline__ float exp2_fast(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
+}
+
+__device__ __forceinline__ void copy16(uint32_t dst, const uint16_t* src, bool ok) {
+  // 16 bytes, or zeros where !ok (nothing is read then)
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(ok ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ uint4 lds16(uint32_t addr) {
+  uint4 v;
+  asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr));
+  return v;
 }
 
 __device__ __forceinline__ uint4 load16(const uint16_t* p, bool ok) {
@@ -68,15 +88,29 @@ __device__ __forceinline__ float2 ld_cluster_f2(uint32_t addr) {
   return v;
 }
 
-// NI: 32-channel groups of the head (D <= 32 NI); NC: 64-channel groups.
+// Shared memory of a CTA: the warps' rings, then (over them) the join.
+template <int DP>
+struct RowsSmem {
+  static constexpr int kBlock = kKeys * DP * 2;               // bytes of a block's keys or values
+  static constexpr int kStages = DP == 128 ? 3 : 6;           // of a warp's ring, K and V each
+  static constexpr int kRing = kWarps * kStages * 2 * kBlock;  // 96 KB
+  static constexpr int kJoin = kWarps * kRows * (DP + 2) * 4 + kRows * (DP + 2) * 4;
+  static constexpr int kBytes = kRing > kJoin ? kRing : kJoin;
+};
+
+// NI: 32-channel groups of the head (D <= 32 NI).
 template <int NI>
 __global__ void __launch_bounds__(kWarps * 32, 2) attention_rows_kernel(const __grid_constant__ AttnArgs a, int splits) {
-  constexpr int NC = (NI + 1) / 2;
+  constexpr int NC = (NI + 1) / 2;  // 64-channel groups
   constexpr int DP = 64 * NC;
-  __shared__ float sm_ml[kWarps][kRows][2];      // running maximum (log2 units) and sum of each warp
-  __shared__ __align__(16) float sm_o[kWarps][kRows][DP];
-  __shared__ float cta_ml[kRows][2];             // the CTA's own, read by the cluster
-  __shared__ __align__(16) float cta_o[kRows][DP];
+  constexpr int kChunks = DP / 8;   // 16-byte groups of a row
+  using M = RowsSmem<DP>;
+  constexpr int ST = M::kStages;
+  extern __shared__ __align__(128) uint8_t dyn[];
+  auto sm_o = reinterpret_cast<float(*)[kRows][DP]>(dyn);                                     // output of each warp
+  auto sm_ml = reinterpret_cast<float(*)[kRows][2]>(dyn + kWarps * kRows * DP * 4);           // its maximum (log2 units), sum
+  auto cta_o = reinterpret_cast<float(*)[DP]>(dyn + kWarps * kRows * (DP + 2) * 4);           // the CTA's own, read by
+  auto cta_ml = reinterpret_cast<float(*)[2]>(dyn + kWarps * kRows * (DP + 2) * 4 + kRows * DP * 4);  // the cluster
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int g = lane >> 2, t = lane & 3;
@@ -114,61 +148,73 @@ __global__ void __launch_bounds__(kWarps * 32, 2) attention_rows_kernel(const __
 #pragma unroll
   for (int j = 0; j < 8 * NC; ++j) o[j][0] = o[j][1] = o[j][2] = o[j][3] = 0.f;
 
-  const int blocks = (len + 15) / 16;
+  const int blocks = (len + kKeys - 1) / kKeys;
   const int stride = splits * kWarps;
-  uint4 kv[2][NI];
-  auto load_k = [&](int blk) {
+  const uint32_t ring = smem_u32(dyn) + uint32_t(warp * ST * 2 * M::kBlock);
+  // The keys and values of block `blk` into ring stage `stage`.
+  auto fetch = [&](int blk, int stage) {
+    const uint32_t base = ring + uint32_t(stage * 2 * M::kBlock);
 #pragma unroll
-    for (int nt = 0; nt < 2; ++nt) {
-      const int key = blk * 16 + nt * 8 + g;
-#pragma unroll
-      for (int i = 0; i < NI; ++i) {
-        const int d = 32 * i + 8 * t;
-        kv[nt][i] = load16(kp + (long long)key * a.k_l + d, key < len && d < a.D);
-      }
+    for (int n = 0; n < kKeys * kChunks / 32; ++n) {
+      const int at = n * 32 + lane, r = at / kChunks, c = at % kChunks;
+      const int key = blk * kKeys + r;
+      const bool ok = key < len && 8 * c < a.D;
+      const uint32_t row = base + uint32_t(r * DP * 2);
+      copy16(row + 16 * (c ^ ((r & 1) << 2)), ok ? kp + (long long)key * a.k_l + 8 * c : kp, ok);
+      copy16(row + M::kBlock + 16 * (c ^ (r & 6)), ok ? vp + (long long)key * a.v_l + 8 * c : vp, ok);
     }
   };
-  int blk = split * kWarps + warp;
-  if (blk < blocks) load_k(blk);
-  for (; blk < blocks; blk += stride) {
+  const int first = split * kWarps + warp;
+#pragma unroll
+  for (int n = 0; n < ST - 1; ++n) {
+    if (first + n * stride < blocks) fetch(first + n * stride, n);
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  }
+  int stage = 0;
+  for (int blk = first; blk < blocks; blk += stride) {
     // Keys of this thread: its score columns and its value rows are the same.
-    bool ok[4];
-    uint4 vv[4][NC];
+    bool ok[2][2];
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      const int key = blk * 16 + 2 * t + (e & 1) + (e >> 1) * 8;
-      ok[e] = key < len && (!mask || mask[key]);
+    for (int nt = 0; nt < 2; ++nt)
 #pragma unroll
-      for (int c = 0; c < NC; ++c) {
-        const int d = 64 * c + 8 * g;
-        vv[e][c] = load16(vp + (long long)key * a.v_l + d, ok[e] && d < a.D);
+      for (int e = 0; e < 2; ++e) {
+        const int key = blk * kKeys + nt * 8 + 2 * t + e;
+        ok[nt][e] = key < len && (!mask || mask[key]);
       }
-    }
+    asm volatile("cp.async.wait_group %0;" ::"n"(ST - 2) : "memory");
+    __syncwarp();  // every lane's copies are in, and its reads of the stage refilled next are done
+    if (blk + (ST - 1) * stride < blocks) fetch(blk + (ST - 1) * stride, stage == 0 ? ST - 1 : stage - 1);
+    asm volatile("cp.async.commit_group;" ::: "memory");
+    const uint32_t kb = ring + uint32_t(stage * 2 * M::kBlock), vb = kb + M::kBlock;
+    stage = stage == ST - 1 ? 0 : stage + 1;
     float s[2][4];
 #pragma unroll
-    for (int nt = 0; nt < 2; ++nt) {
-      s[nt][0] = s[nt][1] = s[nt][2] = s[nt][3] = 0.f;
+    for (int nt = 0; nt < 2; ++nt) s[nt][0] = s[nt][1] = s[nt][2] = s[nt][3] = 0.f;
 #pragma unroll
-      for (int i = 0; i < NI; ++i) {
-        mma_16816(s[nt], q[2 * i][0], q[2 * i][1], q[2 * i][2], q[2 * i][3], kv[nt][i].x, kv[nt][i].y);
-        mma_16816(s[nt], q[2 * i + 1][0], q[2 * i + 1][1], q[2 * i + 1][2], q[2 * i + 1][3], kv[nt][i].z, kv[nt][i].w);
+    for (int i = 0; i < NI; ++i)
+#pragma unroll
+      for (int nt = 0; nt < 2; ++nt) {
+        const uint4 k4 = lds16(kb + uint32_t((nt * 8 + g) * DP * 2) + 16 * ((4 * i + t) ^ ((g & 1) << 2)));
+        mma_16816(s[nt], q[2 * i][0], q[2 * i][1], q[2 * i][2], q[2 * i][3], k4.x, k4.y);
+        mma_16816(s[nt], q[2 * i + 1][0], q[2 * i + 1][1], q[2 * i + 1][2], q[2 * i + 1][3], k4.z, k4.w);
       }
-    }
-    if (blk + stride < blocks) load_k(blk + stride);
     float top[2];
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
+      top[h] = -INFINITY;
 #pragma unroll
       for (int nt = 0; nt < 2; ++nt)
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
           float& v = s[nt][2 * h + e];
-          v = ok[2 * nt + e] ? v * a.scale_log2 : -INFINITY;
+          v = ok[nt][e] ? v * a.scale_log2 : -INFINITY;
+          top[h] = fmaxf(top[h], v);
         }
-      top[h] = fmaxf(fmaxf(s[0][2 * h], s[0][2 * h + 1]), fmaxf(s[1][2 * h], s[1][2 * h + 1]));
-      top[h] = fmaxf(top[h], __shfl_xor_sync(0xffffffffu, top[h], 1));
-      top[h] = fmaxf(top[h], __shfl_xor_sync(0xffffffffu, top[h], 2));
     }
+#pragma unroll
+    for (int x = 1; x <= 2; x *= 2)
+#pragma unroll
+      for (int h = 0; h < 2; ++h) top[h] = fmaxf(top[h], __shfl_xor_sync(0xffffffffu, top[h], x));
     if (__any_sync(0xffffffffu, top[0] > m[0] || top[1] > m[1])) {
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
@@ -182,20 +228,28 @@ __global__ void __launch_bounds__(kWarps * 32, 2) attention_rows_kernel(const __
     }
     uint32_t hi[4], lo[4];  // A fragment of P: (row g | g + 8) x (keys 2t, 2t + 1 | + 8)
 #pragma unroll
-    for (int nt = 0; nt < 2; ++nt)
+    for (int h = 0; h < 2; ++h) {
+      const float base = m[h] == -INFINITY ? 0.f : m[h];
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const float base = m[h] == -INFINITY ? 0.f : m[h];
+      for (int nt = 0; nt < 2; ++nt) {
         const float p0 = exp2_fast(s[nt][2 * h] - base), p1 = exp2_fast(s[nt][2 * h + 1] - base);
         sum[h] += p0 + p1;
         split2(p0, p1, hi[2 * nt + h], lo[2 * nt + h]);
       }
+    }
 #pragma unroll
     for (int c = 0; c < NC; ++c) {
-      const uint32_t* w0 = &vv[0][c].x;
-      const uint32_t* w1 = &vv[1][c].x;
-      const uint32_t* w2 = &vv[2][c].x;
-      const uint32_t* w3 = &vv[3][c].x;
+      uint4 vv[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const int r = 2 * t + (e & 1) + (e >> 1) * 8;
+        vv[e] = lds16(vb + uint32_t(r * DP * 2) + 16 * ((8 * c + g) ^ (r & 6)));
+        if (!ok[e >> 1][e & 1]) vv[e] = make_uint4(0u, 0u, 0u, 0u);
+      }
+      const uint32_t* w0 = &vv[0].x;
+      const uint32_t* w1 = &vv[1].x;
+      const uint32_t* w2 = &vv[2].x;
+      const uint32_t* w3 = &vv[3].x;
 #pragma unroll
       for (int i = 0; i < 4; ++i)
 #pragma unroll
@@ -208,7 +262,9 @@ __global__ void __launch_bounds__(kWarps * 32, 2) attention_rows_kernel(const __
         }
     }
   }
-  // ---- join
+  // ---- join, over the rings once every warp is through with its own
+  asm volatile("cp.async.wait_group 0;" ::: "memory");
+  __syncthreads();
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
     sum[h] += __shfl_xor_sync(0xffffffffu, sum[h], 1);
@@ -286,10 +342,21 @@ __global__ void __launch_bounds__(kWarps * 32, 2) attention_rows_kernel(const __
 
 template <int NI>
 cudaError_t launch_ni(const AttnArgs& a, int splits, cudaStream_t stream) {
+  constexpr int kBytes = RowsSmem<64 * ((NI + 1) / 2)>::kBytes;
+  static thread_local int ready_dev = -1;  // once per device: shared memory above 48 KB, clusters above 8
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (ready_dev != dev) {
+    if ((e = cudaFuncSetAttribute(attention_rows_kernel<NI>, cudaFuncAttributeMaxDynamicSharedMemorySize, kBytes)) != cudaSuccess ||
+        (e = cudaFuncSetAttribute(attention_rows_kernel<NI>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1)) != cudaSuccess)
+      return e;
+    ready_dev = dev;
+  }
   const long long rows = (long long)a.Lq * (a.H / a.Hkv);
   const long long units = (rows + kRows - 1) / kRows * a.Hkv * a.B;
-  return launch_pdl(attention_rows_kernel<NI>, dim3(unsigned(units * splits)), dim3(kWarps * 32), 0, stream, unsigned(splits),
-                    a, splits);
+  return launch_pdl(attention_rows_kernel<NI>, dim3(unsigned(units * splits)), dim3(kWarps * 32), kBytes, stream,
+                    unsigned(splits), a, splits);
 }
 
 }  // namespace
@@ -297,9 +364,9 @@ cudaError_t launch_ni(const AttnArgs& a, int splits, cudaStream_t stream) {
 cudaError_t launch_attention_rows(const AttnArgs& a, int sms, cudaStream_t stream) {
   const long long rows = (long long)a.Lq * (a.H / a.Hkv);
   const long long units = (rows + kRows - 1) / kRows * a.Hkv * a.B;
-  // Split the keys while CTAs are fewer than two per SM and each warp keeps a block of 16 keys.
+  // Split the keys while the CTAs fit the GPU at once (two an SM) and each warp keeps a block.
   int splits = 1;
-  while (splits < 8 && units * splits < 2 * sms && splits * 2 * kWarps <= (a.Lk + 15) / 16) splits *= 2;
+  while (splits < 16 && units * splits * 2 <= 2 * sms && splits * 2 * kWarps <= (a.Lk + kKeys - 1) / kKeys) splits *= 2;
   switch ((a.D + 31) / 32) {
     case 1: return launch_ni<1>(a, splits, stream);
     case 2: return launch_ni<2>(a, splits, stream);

@@ -188,7 +188,6 @@ cudaError_t launch_gated_residual_norm(const ResNormArgs& a, int sms, cudaStream
 
 // Attention of q [B, Lq, H, D] to k, v [B, Lk, Hkv, D] (strides in elements).
 constexpr int kAttnMaxD = 128;
-constexpr int kAttnRowsMax = 64;  // packed query rows of a key-value head up to which the row kernel runs
 struct AttnArgs {
   const uint16_t *q, *k, *v;
   uint16_t* o;

@@ -1129,18 +1129,26 @@ tern_status tern_attention(const tern_attention_args* args, tern_stream_t stream
   a.mask_ld = t.mask_ld;
   a.B = int(t.B), a.Lq = int(t.Lq), a.Lk = int(t.Lk), a.H = int(t.H), a.Hkv = int(t.Hkv), a.D = int(t.D);
   a.scale_log2 = t.scale * 1.44269504088896340736f;
-  if ((t.Lq * (t.H / t.Hkv) + 15) / 16 * t.Hkv * t.B * 8 > INT32_MAX)
+  if ((t.Lq * (t.H / t.Hkv) + 15) / 16 * t.Hkv * t.B * 16 > INT32_MAX)
     return fail(TERN_ERR_UNSUPPORTED_SHAPE, "attention: too many query rows");
   int dev;
   DeviceState* ds;
   tern_status s;
   if ((s = current_device(&dev, &ds)) != TERN_OK) return s;
-  // The row kernel reads K and V once per 16 packed query rows; the tile
-  // kernel once per 256 rows of a head.  (A tensor map has no dimension of
-  // stride 0: tokens that are one broadcast row take the row kernel.)
+  // The row kernel's time grows with its 16-row units times the keys, some 7000
+  // of them a microsecond, behind a shorter start; the tile kernel's with its
+  // rounds over the SMs times the key tiles, 1.4 us each, however few of a
+  // tile's rows there are.  Measured (us, rows | tiles): 1531 keys, 60 units
+  // 10 | 19; 4096 keys, 48 units 32 | 50, 96 units 58 | 50; 512 keys, 24 units
+  // 8.2 | 9.4, 96 units 14 | 9.5; 256 keys, 64 units 5.9 | 7.2.  (A tensor map has
+  // no dimension of stride 0: tokens that are one broadcast row take rows.)
   const bool flat = (t.Lq > 1 && t.q_l == 0) || (t.Lk > 1 && (t.k_l == 0 || t.v_l == 0));
+  const int64_t pairs = (t.Lq + 255) / 256, tile_units = pairs * t.B * t.H;
+  const int64_t row_units = (t.Lq * (t.H / t.Hkv) + 15) / 16 * t.Hkv * t.B;
+  const int64_t rounds = (tile_units + ds->sms - 1) / ds->sms;
+  const bool rows = row_units * t.Lk <= 7000 + ds->sms / 2 * ((t.Lk + 127) / 128 * 128) * rounds;
   cudaError_t e;
-  if (t.Lq * (t.H / t.Hkv) <= kAttnRowsMax || flat || t.Lk == 0) {
+  if (rows || flat || t.Lk == 0) {
     e = launch_attention_rows(a, ds->sms, reinterpret_cast<cudaStream_t>(stream));
   } else {
     AttnTileArgs ta;
@@ -1149,10 +1157,9 @@ tern_status tern_attention(const tern_attention_args* args, tern_stream_t stream
     if ((s = make_heads_map(&ta.tq, q, &ta.q_h, &ta.q_b)) != TERN_OK || (s = make_heads_map(&ta.tk, k, &ta.k_h, &ta.k_b)) != TERN_OK ||
         (s = make_heads_map(&ta.tv, v, &ta.v_h, &ta.v_b)) != TERN_OK)
       return s;
-    const int64_t pairs = (t.Lq + 255) / 256;
-    if (pairs * t.B * t.H > INT32_MAX) return fail(TERN_ERR_UNSUPPORTED_SHAPE, "attention: too many query rows");
+    if (tile_units > INT32_MAX) return fail(TERN_ERR_UNSUPPORTED_SHAPE, "attention: too many query rows");
     ta.pairs = int(pairs);
-    ta.units = int(pairs * t.B * t.H);
+    ta.units = int(tile_units);
     ta.ctas = ds->sms;
     ta.by_pairs = div_by(unsigned(pairs));
     ta.by_heads = div_by(unsigned(t.H));

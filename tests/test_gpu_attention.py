@@ -51,15 +51,20 @@ SIZES = [(1, 1, 1, 1, 1, 8), (1, 1, 1, 1, 1, 128), (1, 1, 512, 24, 24, 128), (2,
          (2, 64, 129, 4, 2, 128), (1, 127, 255, 2, 2, 128), (1, 128, 256, 2, 2, 64), (2, 129, 257, 3, 3, 128),
          (1, 255, 64, 2, 1, 40), (1, 256, 128, 2, 2, 128), (1, 257, 1, 2, 2, 128), (1, 385, 640, 4, 2, 64),
          (1, 1000, 77, 5, 5, 120), (2, 300, 1030, 2, 2, 128), (1, 513, 384, 1, 1, 16)]
+# Enough query rows for the tile kernel: odd and whole tiles, one key tile or many, one query tile in the last pair,
+# grouped heads, more units than SMs.
+TILES = [(2, 129, 257, 12, 12, 128), (1, 257, 300, 12, 3, 64), (1, 384, 128, 16, 16, 128), (3, 128, 64, 20, 10, 72),
+         (1, 1300, 65, 12, 12, 96), (1, 2049, 640, 2, 2, 128), (1, 700, 1, 40, 40, 64), (2, 300, 1030, 10, 5, 128),
+         (1, 4200, 96, 20, 20, 8), (1, 640, 129, 70, 70, 128)]
 
 
-@pytest.mark.parametrize("B,Lq,Lk,H,Hkv,D", SIZES)
+@pytest.mark.parametrize("B,Lq,Lk,H,Hkv,D", SIZES + TILES)
 def test_matches_oracle(B, Lq, Lk, H, Hkv, D):
     q, k, v = inputs(B, Lq, Lk, H, Hkv, D)
     close(tern.attention(q, k, v), q, k, v)
 
 
-@pytest.mark.parametrize("B,Lq,Lk,H,Hkv,D", [s for s in SIZES if s[2] > 1])
+@pytest.mark.parametrize("B,Lq,Lk,H,Hkv,D", [s for s in SIZES if s[2] > 1] + [s for s in TILES[:8] if s[2] > 1])
 @pytest.mark.parametrize("kind", ["len", "mask", "both"])
 def test_masked_keys(B, Lq, Lk, H, Hkv, D, kind):
     """Lengths of zero, one, a part and beyond the end, holes, entries without
@@ -98,7 +103,7 @@ def test_no_keys_no_queries():
     assert tern.attention(q, k, v).shape == (2, 0, 4, 64)
 
 
-@pytest.mark.parametrize("Lq,Lk", [(5, 40), (300, 260)])
+@pytest.mark.parametrize("Lq,Lk", [(5, 40), (300, 260), (900, 140)])
 def test_layouts(Lq, Lk):
     """Slices of fused projections, heads-first tensors, a broadcast of the
     keys over the batch, an output slice whose surroundings stay as they were,
@@ -120,7 +125,7 @@ def test_layouts(Lq, Lk):
     close(tern.attention(qh[0], kh[0], vh[0], key_mask=mask[0]), qh[0], kh[0], vh[0], key_mask=mask[0])
 
 
-@pytest.mark.parametrize("Lq,Lk", [(3, 100), (200, 300)])
+@pytest.mark.parametrize("Lq,Lk", [(3, 100), (200, 300), (1300, 300)])
 def test_scales_and_peaked_scores(Lq, Lk):
     """Scores of hundreds, growing along the keys (each tile raises the
     maximum) and falling; a scale of its own."""
@@ -132,7 +137,7 @@ def test_scales_and_peaked_scores(Lq, Lk):
             close(tern.attention(q, kk, v, scale=scale), q, kk, v, scale=scale)
 
 
-@pytest.mark.parametrize("Lq", [2, 300])
+@pytest.mark.parametrize("Lq", [2, 300, 1700])
 def test_scores_that_are_not_finite_stay_in_their_rows(Lq):
     q, k, v = inputs(1, Lq, 200, 2, 2, 64)
     want = tern.attention(q, k, v)
@@ -143,7 +148,7 @@ def test_scores_that_are_not_finite_stay_in_their_rows(Lq):
     assert torch.equal(got, want)
 
 
-@pytest.mark.parametrize("Lq,Lk", [(4, 300), (260, 300)])
+@pytest.mark.parametrize("Lq,Lk", [(4, 300), (260, 300), (2300, 300)])
 def test_behind_32_bit_offsets(Lq, Lk):
     """Keys and values more than 2^32 bytes apart in one buffer."""
     D, ld = 64, 1 << 24
@@ -155,7 +160,7 @@ def test_behind_32_bit_offsets(Lq, Lk):
     assert torch.equal(tern.attention(q, k, v), tern.attention(q, kk, vv))
 
 
-@pytest.mark.parametrize("Lq,Lk,H", [(1, 700, 8), (40, 700, 8), (520, 300, 2)])
+@pytest.mark.parametrize("Lq,Lk,H", [(1, 700, 8), (40, 700, 8), (520, 300, 2), (1030, 700, 12)])
 def test_same_call_same_bits_other_stream_and_graph(Lq, Lk, H):
     q, k, v = inputs(2, Lq, Lk, H, H // 2, 128)
     n = torch.tensor([Lk, Lk // 2], dtype=torch.int32, device="cuda")
@@ -179,3 +184,25 @@ def test_same_call_same_bits_other_stream_and_graph(Lq, Lk, H):
     torch.cuda.synchronize()
     assert torch.equal(out, tern.attention(q, k, v, kv_len=n))
     close(out, q, k, v, kv_len=n)
+
+
+def test_broadcast_tokens():
+    """Keys and values that are one row for every token (stride 0), and queries likewise."""
+    q, k, v = inputs(1, 1200, 300, 4, 4, 64)
+    k1, v1, q1 = k[:, :1].expand(1, 300, 4, 64), v[:, :1].expand(1, 300, 4, 64), q[:, :1].expand(1, 1200, 4, 64)
+    close(tern.attention(q, k1, v1), q, k1, v1)
+    close(tern.attention(q1, k, v), q1, k, v)
+
+
+def test_two_streams_at_once():
+    """Two calls in flight together, rows and tiles, each on its own inputs."""
+    a, b = inputs(1, 17, 1531, 16, 4, 64), inputs(1, 2049, 640, 4, 4, 128)
+    wa, wb = tern.attention(*a), tern.attention(*b)
+    s, r = torch.cuda.Stream(), torch.cuda.Stream()
+    for st in (s, r):
+        st.wait_stream(torch.cuda.current_stream())
+    oa = [tern.attention(*a, stream=s) for _ in range(8)]
+    ob = [tern.attention(*b, stream=r) for _ in range(8)]
+    torch.cuda.synchronize()
+    assert all(torch.equal(o, wa) for o in oa) and all(torch.equal(o, wb) for o in ob)
+    assert tern.device_status() == 0
