@@ -10,6 +10,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 from typing import Optional, Sequence
 
 import torch
@@ -87,6 +88,10 @@ class GatedResidualNormArgs(ctypes.Structure):
         ("tokens_per_row", ctypes.c_int64)]
 
 
+# The same two layouts for struct.pack, which takes a fifth of the time.
+_ATTENTION = struct.Struct("4P18qfPPq")
+_RESIDUAL_NORM = struct.Struct("4P6qfiPfPiiPfPPqq")
+
 ACT_NONE = 0       # tern_act values
 ACT_GELU_TANH = 1
 
@@ -138,13 +143,13 @@ def lib() -> ctypes.CDLL:
         L.tern_quantize_act_e4m3.restype = st
         L.tern_linear_e4m3.argtypes = [vp, vp, i64, i64, vp, vp, vp, i64, vp, vp]
         L.tern_linear_e4m3.restype = st
-        L.tern_rope_table.argtypes = [vp, i64, ctypes.c_int, ctypes.POINTER(ctypes.c_int), ctypes.c_double, vp, vp]
+        L.tern_rope_table.argtypes = [vp, i64, ctypes.c_int, vp, ctypes.c_double, vp, vp]
         L.tern_rope_table.restype = st
-        L.tern_rope.argtypes = [ctypes.POINTER(RopeTensor), ctypes.c_int, i64, i64, i64, vp, i64, i64, ctypes.c_int, vp]
+        L.tern_rope.argtypes = [vp, ctypes.c_int, i64, i64, i64, vp, i64, i64, ctypes.c_int, vp]
         L.tern_rope.restype = st
-        L.tern_attention.argtypes = [ctypes.POINTER(AttentionArgs), vp]
+        L.tern_attention.argtypes = [vp, vp]
         L.tern_attention.restype = st
-        L.tern_gated_residual_norm.argtypes = [ctypes.POINTER(GatedResidualNormArgs), vp]
+        L.tern_gated_residual_norm.argtypes = [vp, vp]
         L.tern_gated_residual_norm.restype = st
         L.tern_dequantize.argtypes = [vp, vp, i64, i64, vp, vp]
         L.tern_dequantize.restype = st
@@ -431,32 +436,36 @@ def linear_batch_strided(problems: Sequence[dict], stream=None) -> None:
     _check(lib().tern_linear_batch_strided(args, epis, len(problems), _stream(stream)))
 
 
-def _launch_on(ts, stream) -> None:
+def _launch_on(ts, stream) -> int:
     """The library launches on the current device: every tensor has to live
-    there.  With a stream other than the current one, the caching allocator
-    is told that the tensors are in use on it."""
-    dev = -1
+    there.  Returns the raw stream to launch on; where that is not the current
+    one, the caching allocator is told that the tensors are in use on it."""
+    dev = -2
     for t in ts:
         if t is not None:
-            if not t.is_cuda:
-                raise ValueError(f"every tensor must be on the current CUDA device; got one on {t.device}")
-            if dev < 0:
-                dev = torch.cuda.current_device()
-            if t.get_device() != dev:
-                raise ValueError(f"every tensor must be on the current CUDA device ({dev}); got one on {t.device}")
-    if stream is not None and dev >= 0:
-        if stream.device.index != dev:
-            raise ValueError(f"the stream belongs to device {stream.device.index}, the current one is {dev}")
-        if stream != torch.cuda.current_stream():
-            for t in ts:
-                if t is not None:
-                    t.record_stream(stream)
+            d = t.get_device()  # -1 on the host
+            if d != dev:
+                if d < 0 or dev >= 0 or d != torch.cuda.current_device():
+                    raise ValueError(f"every tensor must be on the current CUDA device; got one on {t.device}")
+                dev = d
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(dev)
+    if stream.device.index != dev:
+        raise ValueError(f"the stream belongs to device {stream.device.index}, the tensors to {dev}")
+    if stream != torch.cuda.current_stream():
+        for t in ts:
+            if t is not None:
+                t.record_stream(stream)
+    return stream.cuda_stream
 
 
-def _bf16(name: str, t: torch.Tensor, dims) -> None:
-    if t.dtype is not torch.bfloat16 or t.dim() not in dims or (t.stride(-1) != 1 and t.shape[-1] > 1):
+def _bf16(name: str, t: torch.Tensor, dims) -> tuple:
+    """t's strides, once it is known to be bf16 with adjacent channels."""
+    s = t.stride()
+    if t.dtype is not torch.bfloat16 or len(s) not in dims or (s[-1] != 1 and t.shape[-1] > 1):
         raise ValueError(f"{name} must be bf16 with {' or '.join(map(str, dims))} dimensions and adjacent channels; got "
-                         f"{t.dtype}, shape {tuple(t.shape)}, strides {t.stride()}")
+                         f"{t.dtype}, shape {tuple(t.shape)}, strides {s}")
+    return s
 
 
 def rope_table(ids: torch.Tensor, axes: Sequence[int], theta: float = 10000.0, out: Optional[torch.Tensor] = None,
@@ -466,18 +475,16 @@ def rope_table(ids: torch.Tensor, axes: Sequence[int], theta: float = 10000.0, o
     it turning by ids[:, a] * theta^(-2 i / axes[a]).  The table that `rope`
     and (with P = 64) the linears' rope_cs take."""
     n = len(axes)
-    if ids.dtype != torch.float32 or ids.dim() != 2 or ids.shape[1] != n or not ids.is_contiguous():
-        raise ValueError(f"ids must be contiguous fp32 [L, {n}], got {ids.dtype} {tuple(ids.shape)}")
-    L, P = ids.shape[0], sum(axes) // 2
+    shape = ids.shape
+    if ids.dtype is not torch.float32 or len(shape) != 2 or shape[1] != n or not ids.is_contiguous():
+        raise ValueError(f"ids must be contiguous fp32 [L, {n}], got {ids.dtype} {tuple(shape)}")
+    L, P = shape[0], sum(axes) // 2
+    raw = _launch_on((ids, out), stream)
     if out is None:
-        _launch_on((ids,), stream)
         out = _empty(L, P, 2, dtype=torch.float32, device=ids.device, stream=stream)
-    else:
-        if out.dtype != torch.float32 or out.shape != (L, P, 2) or not out.is_contiguous():
-            raise ValueError(f"out must be contiguous fp32 [{L}, {P}, 2]")
-        _launch_on((ids, out), stream)
-    _check(lib().tern_rope_table(_ptr(ids), L, n, (ctypes.c_int * max(n, 1))(*axes), float(theta), _ptr(out),
-                                 _stream(stream)))
+    elif out.dtype is not torch.float32 or out.shape != (L, P, 2) or not out.is_contiguous():
+        raise ValueError(f"out must be contiguous fp32 [{L}, {P}, 2]")
+    _check(lib().tern_rope_table(ids.data_ptr(), L, n, struct.pack(f"{n}i", *axes), float(theta), out.data_ptr(), raw))
     return out
 
 
@@ -492,28 +499,31 @@ def rope(xs: Sequence[torch.Tensor], cs: torch.Tensor, halves: bool = False,
     if not xs:
         return []
     shape = xs[0].shape
+    strides = []
     for x in xs:
-        _bf16("x", x, (3, 4))
-        if x.dim() != len(shape) or x.shape[:-2] != shape[:-2] or x.shape[-1] != shape[-1]:
+        strides.append(_bf16("x", x, (3, 4)))
+        sh = x.shape
+        if len(sh) != len(shape) or sh[:-2] != shape[:-2] or sh[-1] != shape[-1]:
             raise ValueError("the tensors must share their tokens and head size")
-    if cs.dtype != torch.float32 or cs.dim() != 3 or cs.shape[2] != 2 or not cs.is_contiguous():
+    table = cs.shape
+    if cs.dtype is not torch.float32 or len(table) != 3 or table[2] != 2 or not cs.is_contiguous():
         raise ValueError("cs must be contiguous fp32 [rows, P, 2]")
-    _launch_on((*xs, cs, *(outs or ())), stream)
+    raw = _launch_on((*xs, cs, *(outs or ())), stream)
     if outs is None:
         outs = [_empty_as(x, stream) for x in xs]
     elif len(outs) != len(xs):
         raise ValueError("one output per tensor")
-    arr = (RopeTensor * len(xs))()
-    for i, (x, y) in enumerate(zip(xs, outs)):
+    args = []
+    for x, y, sx in zip(xs, outs, strides):
         if y.shape != x.shape:
             raise ValueError("an output has its input's shape")
-        _bf16("out", y, (3, 4))
-        sx, sy = x.stride(), y.stride()
-        arr[i] = RopeTensor(x.data_ptr(), y.data_ptr(), x.shape[-2], sx[0] if len(sx) == 4 else 0, sx[-3], sx[-2],
-                            sy[0] if len(sy) == 4 else 0, sy[-3], sy[-2])
+        sy = _bf16("out", y, (3, 4))
+        if len(sx) == 3:
+            sx, sy = (0, *sx), (0, *sy)
+        args += (x.data_ptr(), y.data_ptr(), x.shape[-2], *sx[:3], *sy[:3])
     B, L = (shape[0], shape[1]) if len(shape) == 4 else (1, shape[0])
-    _check(lib().tern_rope(arr, len(xs), B, L, shape[-1], _ptr(cs), cs.shape[0], cs.shape[1], 1 if halves else 0,
-                           _stream(stream)))
+    _check(lib().tern_rope(struct.pack("2P7q" * len(xs), *args), len(xs), B, L, shape[-1], cs.data_ptr(), table[0],
+                           table[1], 1 if halves else 0, raw))
     return list(outs)
 
 
@@ -526,37 +536,41 @@ def attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, scale: Optional
     1 / sqrt(D).  kv_len int32 [B] and key_mask bool or uint8 [B, Lk] (without
     B: [1] and [Lk]) say which keys count; a batch entry without one gives
     zeros.  Returns [B, Lq, H, D] (contiguous, or `out`)."""
-    nd = q.dim()
-    for name, t in (("q", q), ("k", k), ("v", v)):
-        _bf16(name, t, (3, 4))
-        if t.dim() != nd:
-            raise ValueError("q, k and v must all have a batch dimension, or none")
-    B, (Lq, H, D), (Lk, Hkv) = (q.shape[0] if nd == 4 else 1), q.shape[-3:], k.shape[-3:-1]
-    if k.shape != v.shape or k.shape[-1] != D or (nd == 4 and k.shape[0] != B):
-        raise ValueError(f"q {tuple(q.shape)}, k {tuple(k.shape)} and v {tuple(v.shape)} do not fit")
-    if kv_len is not None and (kv_len.dtype != torch.int32 or kv_len.shape != (B,) or not kv_len.is_contiguous()):
-        raise ValueError(f"kv_len must be contiguous int32 [{B}]")
-    mask_ld = 0
+    sq, sk, sv = _bf16("q", q, (3, 4)), _bf16("k", k, (3, 4)), _bf16("v", v, (3, 4))
+    nd = len(sq)
+    if len(sk) != nd or len(sv) != nd:
+        raise ValueError("q, k and v must all have a batch dimension, or none")
+    qs, ks = q.shape, k.shape
+    if nd == 4:
+        (B, Lq, H, D), (Bk, Lk, Hkv, Dk) = qs, ks
+    else:
+        (Lq, H, D), (Lk, Hkv, Dk), B, Bk = qs, ks, 1, 1
+        sq, sk, sv = (0, *sq), (0, *sk), (0, *sv)
+    if v.shape != ks or Dk != D or Bk != B:
+        raise ValueError(f"q {tuple(qs)}, k {tuple(ks)} and v {tuple(v.shape)} do not fit")
+    lens = mask = mask_ld = 0
+    if kv_len is not None:
+        if kv_len.dtype is not torch.int32 or kv_len.shape != (B,) or not kv_len.is_contiguous():
+            raise ValueError(f"kv_len must be contiguous int32 [{B}]")
+        lens = kv_len.data_ptr()
     if key_mask is not None:
         if (key_mask.dtype not in (torch.bool, torch.uint8) or key_mask.shape != ((B, Lk) if nd == 4 else (Lk,))
                 or (Lk > 1 and key_mask.stride(-1) != 1)):
             raise ValueError(f"key_mask must be bool or uint8 {'[B, Lk]' if nd == 4 else '[Lk]'} with adjacent keys")
-        mask_ld = key_mask.stride(0) if nd == 4 else 0
-    _launch_on((q, k, v, kv_len, key_mask, out), stream)
+        mask, mask_ld = key_mask.data_ptr(), key_mask.stride(0) if nd == 4 else 0
+    raw = _launch_on((q, k, v, kv_len, key_mask, out), stream)
     if out is None:
         out = _empty_as(q, stream)
+        so = out.stride()
     else:
-        _bf16("out", out, (nd,))
-        if out.shape != q.shape:
+        so = _bf16("out", out, (nd,))
+        if out.shape != qs:
             raise ValueError("out has q's shape")
-    sq, sk, sv, so = (t.stride() for t in (q, k, v, out))
     if nd == 3:
-        sq, sk, sv, so = ((0, *s) for s in (sq, sk, sv, so))
-    a = AttentionArgs(q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(), B, Lq, Lk, H, Hkv, D, *sq[:3], *sk[:3],
-                      *sv[:3], *so[:3], D ** -0.5 if scale is None else scale,
-                      None if kv_len is None else kv_len.data_ptr(),
-                      None if key_mask is None else key_mask.data_ptr(), mask_ld)
-    _check(lib().tern_attention(ctypes.byref(a), _stream(stream)))
+        so = (0, *so)
+    _check(lib().tern_attention(
+        _ATTENTION.pack(q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(), B, Lq, Lk, H, Hkv, D, *sq[:3], *sk[:3],
+                        *sv[:3], *so[:3], D ** -0.5 if scale is None else scale, lens, mask, mask_ld), raw))
     return out
 
 
@@ -574,48 +588,45 @@ def gated_residual_norm(x: torch.Tensor, o: torch.Tensor, *, gate: Optional[torc
     e.g. slices of a modulation output; the norms are NORM_* values.  x_out
     may be x, h may be o (or the reverse).  Returns (x_out, h); h is None, and
     not computed, where neither a pre norm, scale and shift, nor h is given."""
-    _bf16("x", x, (2,))
-    _bf16("o", o, (2,))
-    M, K = x.shape
-    if o.shape != x.shape:
+    sx, so = _bf16("x", x, (2,)), _bf16("o", o, (2,))
+    shape = x.shape
+    M, K = shape
+    if o.shape != shape:
         raise ValueError("x and o must have one shape")
     T = max(M, 1) if tokens_per_row is None else int(tokens_per_row)
     G = -(-M // T) if T > 0 else 0
     mod_ld = K
-    mods = [(n, t) for n, t in (("gate", gate), ("scale", scale), ("shift", shift)) if t is not None]
-    for name, t in mods:
-        _bf16(name, t, (1, 2))
-        if t.shape[-1] != K or (t.shape[0] if t.dim() == 2 else 1) < G:
-            raise ValueError(f"{name} holds fewer than the {G} modulation rows of {K} values that {M} rows at {T} tokens "
-                             "per row need")
-    if G > 1:
-        mod_ld = mods[0][1].stride(0) if mods else K
-        if any(t.stride(0) != mod_ld for _, t in mods):
-            raise ValueError("gate, scale and shift rows must be the same distance apart")
+    apart = None
+    for name, t in (("gate", gate), ("scale", scale), ("shift", shift)):
+        if t is not None:
+            s = _bf16(name, t, (1, 2))
+            sh = t.shape
+            if sh[-1] != K or (sh[0] if len(sh) == 2 else 1) < G:
+                raise ValueError(f"{name} holds fewer than the {G} modulation rows of {K} values that {M} rows at {T} tokens "
+                                 "per row need")
+            if G > 1:
+                if apart is not None and s[0] != apart:
+                    raise ValueError("gate, scale and shift rows must be the same distance apart")
+                apart = mod_ld = s[0]
     for name, t in (("post_weight", post_weight), ("pre_weight", pre_weight)):
         if t is not None:
             _bf16(name, t, (1,))
             if t.shape[0] != K:
                 raise ValueError(f"{name} must hold {K} values")
-    for name, t in (("x_out", x_out), ("h", h)):
-        if t is not None:
-            _bf16(name, t, (2,))
-            if t.shape != x.shape:
-                raise ValueError(f"{name} has x's shape")
-    _launch_on((x, o, gate, scale, shift, post_weight, pre_weight, x_out, h), stream)
+    raw = _launch_on((x, o, gate, scale, shift, post_weight, pre_weight, x_out, h), stream)
     if x_out is None:
         x_out = _empty_as(x, stream)
     if h is None and (pre_norm != NORM_NONE or scale is not None or shift is not None):
         h = _empty_as(x, stream)
-    ld = lambda t: K if t is None or M <= 1 else t.stride(0)  # noqa: E731
-    a = GatedResidualNormArgs(x.data_ptr(), o.data_ptr(), x_out.data_ptr(), None if h is None else h.data_ptr(), M, K,
-                              ld(x), ld(o), ld(x_out), ld(h), residual_scale, post_norm,
-                              None if post_weight is None else post_weight.data_ptr(), post_eps,
-                              None if gate is None else gate.data_ptr(), 1 if gate_tanh else 0, pre_norm,
-                              None if pre_weight is None else pre_weight.data_ptr(), pre_eps,
-                              None if scale is None else scale.data_ptr(), None if shift is None else shift.data_ptr(),
-                              mod_ld, T)
-    _check(lib().tern_gated_residual_norm(ctypes.byref(a), _stream(stream)))
+    sxo, sh = _bf16("x_out", x_out, (2,)), (K, 1) if h is None else _bf16("h", h, (2,))
+    if x_out.shape != shape or (h is not None and h.shape != shape):
+        raise ValueError("x_out and h have x's shape")
+    lds = (sx[0], so[0], sxo[0], sh[0]) if M > 1 else (K, K, K, K)
+    p = lambda t: 0 if t is None else t.data_ptr()  # noqa: E731
+    _check(lib().tern_gated_residual_norm(
+        _RESIDUAL_NORM.pack(x.data_ptr(), o.data_ptr(), x_out.data_ptr(), p(h), M, K, *lds, residual_scale, post_norm,
+                            p(post_weight), post_eps, p(gate), 1 if gate_tanh else 0, pre_norm, p(pre_weight), pre_eps,
+                            p(scale), p(shift), mod_ld, T), raw))
     return x_out, h
 
 

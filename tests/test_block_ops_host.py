@@ -4,6 +4,7 @@ before anything is launched (fake pointers, never dereferenced)."""
 from __future__ import annotations
 
 import ctypes
+import struct
 
 import numpy as np
 import pytest
@@ -184,6 +185,16 @@ def test_gated_residual_norm_rejects(L):
     assert _norm(L, h=F + 0x400000) == INVALID and _norm(L, x_out=F + 0x500000) == INVALID  # a modulation row
     assert _norm(L, post_weight=F + 0x200100) == INVALID
     assert _norm(L, M=0, x=None, o=None, x_out=None) == OK
+
+
+def test_packed_layouts_are_the_structures():
+    """The binding packs two argument blocks without ctypes: byte for byte the ctypes mirrors of the header's."""
+    v = list(range(1, 23)) + [0.5, 24, 25, 26]
+    assert tern._ATTENTION.pack(*v) == bytes(tern.AttentionArgs(*v))
+    v = list(range(1, 11)) + [0.5, 12, 13, 1.5, 15, 16, 17, 18, 2.5, 20, 21, 22, 23]
+    assert tern._RESIDUAL_NORM.pack(*v) == bytes(tern.GatedResidualNormArgs(*v))
+    v = list(range(1, 10))
+    assert struct.pack("2P7q", *v) == bytes(tern.RopeTensor(*v))
 
 
 # ------------------------------------------------------------ binding refusals
