@@ -22,6 +22,16 @@ attention output overwrites the v columns, so the second linear reads
 vectors of every block depend only on vec: one batch of GEMVs computes them
 all before the first block.
 
+With an encoder's states as context (image features beside the prompt, for
+instance), the image tokens of every double block also attend to them: the
+states' keys and values come from a ternary projection of their own, the
+queries are the block's normalised ones before rotation, and what comes back
+is normalised and enters the stream through a tanh gate together with the
+norm before the MLP.  Rotation then follows as an operation of its own
+instead of in the projection's epilogue.  All of it runs in the library
+(``tern.rope_table``, ``tern.attention``, ``tern.rope``,
+``tern.gated_residual_norm``); without context nothing changes.
+
 ``dense_forward`` runs the same blocks with bf16 dense weights (the
 dequantised ternary weights) through cuBLAS and torch's unfused operations:
 the bf16 model that the pages compare against, for latency context.
@@ -105,7 +115,9 @@ class TernaryFlux:
     """The block stack of a FLUX.1-shaped transformer with ternary linears.
 
     ``weights`` maps ("double" | "single", index) to the bf16 parameters of
-    ``workloads.flux_block_weights``; every linear is quantised with
+    ``workloads.flux_block_weights``, and ("context", index), where double
+    block ``index`` attends to an encoder's states, to those of
+    ``workloads.flux_context_weights``; every linear is quantised with
     ``tern.quantize_pack`` at construction (eps = workloads.EPS) and only the
     codes, scales and biases are kept.  With ``stream`` given, construction
     and every forward run on it, the torch operations included, after the
@@ -137,6 +149,14 @@ class TernaryFlux:
                     q[s + "norm_w"] = _qk_norm_weight(p[s + "q_norm"].to(self.device), p[s + "k_norm"].to(self.device),
                                                       C, N)
                 self.blocks[(kind, i)] = q
+        self.context = {}
+        for i in range(cfg.n_double):
+            p = weights.get(("context", i)) if weights is not None else None
+            if p is not None:
+                W, b = p["kv"]
+                packed, scales = tern.quantize_pack(W.to(self.device), workloads.EPS, stream=stream)
+                self.context[i] = {"kv": (packed, scales, b.to(self.device)), "norm": p["norm"].to(self.device),
+                                   "gate": p["gate"].to(self.device)}
 
     def _lin(self, q, x, y, **epi):
         packed, scales, b = q
@@ -157,9 +177,33 @@ class TernaryFlux:
             tern.linear_batch(probs[g:g + 15], stream=self.stream)
         return outs
 
-    def double_block(self, i: int, img: torch.Tensor, txt: torch.Tensor, mods, cs, buf):
+    def context_kv(self, context: torch.Tensor) -> Dict:
+        """Keys and values [Lc, 2C] of the encoder's states context [Lc, dim]
+        for every double block that attends to them, in batched launches."""
+        outs = {i: torch.empty(context.shape[0], c["kv"][1].shape[0], dtype=torch.bfloat16, device=self.device)
+                for i, c in self.context.items()}
+        probs = [self._lin(c["kv"], context, outs[i]) for i, c in self.context.items()]
+        for g in range(0, len(probs), 15):
+            tern.linear_batch(probs[g:g + 15], stream=self.stream)
+        return outs
+
+    def attend_context(self, qkv: torch.Tensor, Lt: int, kv: torch.Tensor, kv_len, cs: torch.Tensor, out: torch.Tensor):
+        """out [Li, C]: attention of the image tokens' queries, normalised and
+        not yet rotated in qkv, to the encoder's states; then rotates q and k
+        of every token in place."""
+        C = self.cfg.hidden
+        H = self.cfg.heads
+        heads = lambda t: t.view(t.shape[0], H, HEAD_DIM)  # noqa: E731
+        tern.attention(heads(qkv[Lt:, :C]), heads(kv[:, :C]), heads(kv[:, C:]), kv_len=kv_len, out=heads(out),
+                       stream=self.stream)
+        qk = [heads(qkv[:, :C]), heads(qkv[:, C:2 * C])]
+        tern.rope(qk, cs, outs=qk, stream=self.stream)
+
+    def double_block(self, i: int, img: torch.Tensor, txt: torch.Tensor, mods, cs, buf, kv=None, kv_len=None):
         """Updates img [Li, C] and txt [Lt, C] in place; cs [Lt + Li, 64, 2]
-        the rotary (cos, sin) of every token row (text first)."""
+        the rotary (cos, sin) of every token row (text first).  With kv [Lc,
+        2C] (and its valid length kv_len [1] int32, or None) the image tokens
+        attend to the encoder's states as well."""
         C = self.cfg.hidden
         q = self.blocks[("double", i)]
         Lt = txt.shape[0]
@@ -170,8 +214,11 @@ class TernaryFlux:
             xm = buf[s + "xm"]
             tern.adaln_modulate(x, m[:, C:2 * C], m[:, :C], LN_EPS, out=xm, stream=self.stream)
             probs.append(self._lin(q[s + "qkv"], xm, qkv[rows], norm_col0=0, norm_col1=2 * C,
-                                   norm_weight=q[s + "norm_w"], norm_eps=QK_EPS, rope_cs=cs[rows]))
+                                   norm_weight=q[s + "norm_w"], norm_eps=QK_EPS,
+                                   rope_cs=cs[rows] if kv is None else None))
         tern.linear_batch_epilogue(probs, stream=self.stream)
+        if kv is not None:
+            self.attend_context(qkv, Lt, kv, kv_len, cs, buf["ctx"])
         o = attention(qkv, C)  # [H, L, D]; q and k rotated in the epilogue
         att = buf["att"]
         att.view(att.shape[0], -1, HEAD_DIM).copy_(o.transpose(0, 1))
@@ -184,7 +231,14 @@ class TernaryFlux:
         for s, x in (("img.", img), ("txt.", txt)):
             m = mods[("double", i, s)]
             xm = buf[s + "xm"]
-            tern.adaln_modulate(x, m[:, 4 * C:5 * C], m[:, 3 * C:4 * C], LN_EPS, out=xm, stream=self.stream)
+            if kv is not None and s == "img.":
+                c = self.context[i]
+                tern.gated_residual_norm(x, buf["ctx"], gate=c["gate"], gate_tanh=True, post_norm=tern.NORM_RMS,
+                                         post_weight=c["norm"], post_eps=QK_EPS, pre_norm=tern.NORM_LAYER, pre_eps=LN_EPS,
+                                         scale=m[:, 4 * C:5 * C], shift=m[:, 3 * C:4 * C], x_out=x, h=xm,
+                                         stream=self.stream)
+            else:
+                tern.adaln_modulate(x, m[:, 4 * C:5 * C], m[:, 3 * C:4 * C], LN_EPS, out=xm, stream=self.stream)
             probs.append(self._lin(q[s + "mlp_up"], xm, buf[s + "h"], act=tern.ACT_GELU_TANH, act_col0=0))
         tern.linear_batch_epilogue(probs, stream=self.stream)
         probs = [self._lin(q[s + "mlp_down"], buf[s + "h"], x, residual=x, gate=mods[("double", i, s)][0, 5 * C:])
@@ -210,24 +264,39 @@ class TernaryFlux:
         C, Fm = self.cfg.hidden, self.cfg.mlp
         e = lambda *shape: torch.empty(*shape, dtype=torch.bfloat16, device=self.device)  # noqa: E731
         return {"qkv": e(Lt + Li, 3 * C), "att": e(Lt + Li, C), "img.xm": e(Li, C), "txt.xm": e(Lt, C),
-                "img.h": e(Li, Fm), "txt.h": e(Lt, Fm), "xm": e(Lt + Li, C), "z": e(Lt + Li, 3 * C + Fm)}
+                "img.h": e(Li, Fm), "txt.h": e(Lt, Fm), "xm": e(Lt + Li, C), "z": e(Lt + Li, 3 * C + Fm),
+                **({"ctx": e(Li, C)} if self.context else {})}
 
     def forward(self, img: torch.Tensor, txt: torch.Tensor, vec: torch.Tensor, ids: torch.Tensor,
-                n_double: Optional[int] = None, n_single: Optional[int] = None) -> torch.Tensor:
+                n_double: Optional[int] = None, n_single: Optional[int] = None,
+                context: Optional[torch.Tensor] = None, context_len: Optional[torch.Tensor] = None) -> torch.Tensor:
         """All blocks on img [Li, C], txt [Lt, C], vec [1, C] (bf16 on the
         device), token positions ids [Lt + Li, 3]; returns the stream
         [Lt + Li, C] after the last single block (text rows first).  The
-        inputs are not modified."""
+        inputs are not modified.  context [Lc, dim] (bf16 on the device): an
+        encoder's states for the double blocks that have weights for them, of
+        which the first context_len ([1] int32 on the device; all of them
+        where None) count."""
+        if context is not None and not self.context:
+            raise ValueError("the model has no weights to attend to an encoder's states")
+        if context_len is not None and context is None:
+            raise ValueError("context_len without context")
         with _on(self.stream):
-            return self._forward(img, txt, vec, ids, n_double, n_single)
+            return self._forward(img, txt, vec, ids, n_double, n_single, context, context_len)
 
-    def _forward(self, img, txt, vec, ids, n_double, n_single):
+    def _forward(self, img, txt, vec, ids, n_double, n_single, context=None, context_len=None):
         cfg = self.cfg
         nd = cfg.n_double if n_double is None else n_double
         ns = cfg.n_single if n_single is None else n_single
         Li, Lt = img.shape[0], txt.shape[0]
-        cos, sin = rope_cos_sin(ids.to(self.device))
-        cs = torch.stack([cos, sin], dim=-1).contiguous()  # [L, 64, 2], read by the q/k epilogues
+        kv = {}
+        if context is None:
+            cos, sin = rope_cos_sin(ids.to(self.device))
+            cs = torch.stack([cos, sin], dim=-1).contiguous()  # [L, 64, 2], read by the q/k epilogues
+        else:
+            cs = tern.rope_table(ids.to(self.device, torch.float32).contiguous(), workloads.ROPE_AXES, ROPE_THETA,
+                                 stream=self.stream)
+            kv = self.context_kv(context)
         mods = self.modulations(vec)
         buf = self.buffers(Li, Lt)
         x = torch.empty(Lt + Li, cfg.hidden, dtype=torch.bfloat16, device=self.device)
@@ -235,7 +304,7 @@ class TernaryFlux:
         x[Lt:].copy_(img)
         img_s, txt_s = x[Lt:], x[:Lt]  # the streams live in their rows of x
         for i in range(nd):
-            self.double_block(i, img_s, txt_s, mods, cs, buf)
+            self.double_block(i, img_s, txt_s, mods, cs, buf, kv.get(i), context_len if i in kv else None)
         for i in range(ns):
             self.single_block(i, x, mods, cs, buf)
         return x
@@ -267,14 +336,15 @@ def io_layers_in(io: Dict, img_lat, txt_ctx, pooled, t: float, guidance: float):
 
 
 def model_forward(model: "TernaryFlux", io: Dict, img_lat, txt_ctx, pooled, t: float, guidance: float, ids,
-                  n_double=None, n_single=None) -> torch.Tensor:
+                  n_double=None, n_single=None, context=None, context_len=None) -> torch.Tensor:
     """The whole transformer: the bf16 input layers, every block through the
     library, and the final layer (adaLN modulation row from SiLU(vec) in
     bf16, layer norm and modulation of the image tokens by the library's
-    adaLN pass, the bf16 output projection).  Returns [Li, in_channels]."""
+    adaLN pass, the bf16 output projection).  context and context_len as
+    TernaryFlux.forward takes them.  Returns [Li, in_channels]."""
     with _on(model.stream):
         img, txt, vec = io_layers_in(io, img_lat, txt_ctx, pooled, t, guidance)
-        x = model.forward(img, txt, vec, ids, n_double, n_single)
+        x = model.forward(img, txt, vec, ids, n_double, n_single, context, context_len)
         C = model.cfg.hidden
         mod = F.linear(F.silu(vec), *io["final.mod"])  # [shift | scale]
         h = tern.adaln_modulate(x[txt.shape[0]:], mod[:, C:], mod[:, :C], LN_EPS, stream=model.stream)

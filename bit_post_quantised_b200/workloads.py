@@ -215,6 +215,22 @@ def flux_block_weights(cfg: FluxConfig, kind: str, index: int, device=None):
     return p
 
 
+def flux_context_weights(cfg: FluxConfig, index: int, dim: int, device=None):
+    """Seeded bf16 parameters by which double block `index` attends to an
+    encoder's states of `dim` channels: their key and value projection (W
+    [2C, dim] ~ N(0, 0.02), b [2C] ~ N(0, 0.01)), the RMS norm weight of what
+    comes back ([C] ~ 1 + N(0, 0.1)) and the gate's logits ([C] ~ N(0, 0.5))."""
+    dev = torch.device("cpu") if device is None else torch.device(device)
+    gen = torch.Generator(device=dev).manual_seed(cfg.seed * 1000003 + 2000 + index)
+
+    def normal(shape, std, mean=0.0):
+        return (torch.randn(shape, generator=gen, device=dev) * std + mean).to(torch.bfloat16)
+
+    C = cfg.hidden
+    return {"kv": (normal((2 * C, dim), W_STD), normal((2 * C,), B_STD)), "norm": normal((C,), NORM_W_STD, 1.0),
+            "gate": normal((C,), 0.5)}
+
+
 def flux_inputs(cfg: FluxConfig, seed: int = 5):
     """Seeded CPU inputs of the block stack: img [Li, C], txt [Lt, C], vec
     [1, C] (bf16, N(0, 1)) and the token positions ids [Lt + Li, 3] (text

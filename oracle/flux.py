@@ -137,10 +137,22 @@ def _attend(qkv: np.ndarray, hidden: int) -> np.ndarray:
     return bf16(_tokens(attention(q, k, v)))
 
 
-def double_block(img: np.ndarray, txt: np.ndarray, vec: np.ndarray, p: dict, angles: np.ndarray):
+def _turned(x: np.ndarray, angles: np.ndarray) -> np.ndarray:
+    """[L, H * D] heads rotated, rounded to bf16."""
+    return bf16(_tokens(apply_rope(_heads(x), angles)))
+
+
+def double_block(img: np.ndarray, txt: np.ndarray, vec: np.ndarray, p: dict, angles: np.ndarray, context=None):
     """FLUX.1's double-stream block.  img [Li, C], txt [Lt, C] and vec [1, C]
     are bf16 values in float64; angles [Lt + Li, 64] for the text tokens
-    followed by the image tokens.  Returns (img, txt) as bf16 values."""
+    followed by the image tokens.  Returns (img, txt) as bf16 values.
+
+    context: an encoder's (valid) states [Lc, dim], to which the image tokens
+    attend with their normalised queries before rotation; p then also holds
+    "ctx.kv" (a ternary linear [2C, dim]), "ctx.norm" and "ctx.gate" (bf16 bit
+    patterns [C]): img += tanh(gate) * RMS-norm(attention) * norm, in one step
+    with the modulated layer norm before the MLP, which reads the sum before
+    it is rounded."""
     hidden = img.shape[1]
     y = bf16(silu(vec))
     out = {}
@@ -153,12 +165,27 @@ def double_block(img: np.ndarray, txt: np.ndarray, vec: np.ndarray, p: dict, ang
     for s, x, ang in (("img", img, angles[lt:]), ("txt", txt, angles[:lt])):
         sh1, sc1 = mods[s][0], mods[s][1]
         xm = bf16(adaln_modulate(bits(x), bits(sc1[None]), bits(sh1[None]), LN_EPS))
-        qkv[s] = _qk_normed(bf16(_lin(xm, p[s + ".qkv"])), p[s + ".q_norm"], p[s + ".k_norm"], hidden, ang)
+        y1 = bf16(_lin(xm, p[s + ".qkv"]))
+        if context is None:
+            qkv[s] = _qk_normed(y1, p[s + ".q_norm"], p[s + ".k_norm"], hidden, ang)
+        else:
+            qk = bf16(rms_norm_groups(y1[:, :2 * hidden], 0, 2 * hidden, QK_EPS,
+                                      _qk_norm_weight(p[s + ".q_norm"], p[s + ".k_norm"], hidden)))
+            if s == "img":
+                kv = bf16(_lin(context, p["ctx.kv"]))
+                seen = bf16(_tokens(attention(_heads(qk[:, :hidden]), _heads(kv[:, :hidden]), _heads(kv[:, hidden:]))))
+            qkv[s] = np.concatenate([_turned(qk[:, :hidden], ang), _turned(qk[:, hidden:], ang), y1[:, 2 * hidden:]], axis=1)
     att = _attend(np.concatenate([qkv["txt"], qkv["img"]], axis=0), hidden)
     for s, x, a in (("img", img, att[lt:]), ("txt", txt, att[:lt])):
         sh1, sc1, g1, sh2, sc2, g2 = mods[s]
         x1 = bf16(_lin(a, p[s + ".proj"], residual_bits=bits(x), gate_bits=bits(g1)))
         xm = bf16(adaln_modulate(bits(x1), bits(sc2[None]), bits(sh2[None]), LN_EPS))
+        if context is not None and s == "img":
+            r = seen / np.sqrt((seen ** 2).mean(axis=1, keepdims=True) + QK_EPS) * from_bits(p["ctx.norm"])
+            r = x1 + np.tanh(from_bits(p["ctx.gate"])) * r
+            c = r - r.mean(axis=1, keepdims=True)
+            xm = bf16(c / np.sqrt((c ** 2).mean(axis=1, keepdims=True) + LN_EPS) * (1 + sc2) + sh2)
+            x1 = bf16(r)
         T, sc, b = p[s + ".mlp_up"]
         h = bf16(linear_act(bits(xm), T, sc, b, ACT_GELU_TANH, 0))
         out[s] = bf16(_lin(h, p[s + ".mlp_down"], residual_bits=bits(x1), gate_bits=bits(g2)))
