@@ -415,19 +415,35 @@ __global__ void __launch_bounds__(kThreads, 1) attention_tile_kernel(const __gri
       // ---------------------------------------------------- MMA issuer
       const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
       bool ok = true;
-      auto wait = [&](uint64_t* bar, int parity) {
-        return bool(__all_sync(0xffffffffu, bar_wait(smem_u32(bar), parity, lim, st)));
+      // Every lane with `need` waits for a barrier of its own: one poll, of
+      // some 150 cycles, for all that a step needs.
+      auto wait_all = [&](uint32_t bar, uint32_t parity, bool need) {
+        bool done = !need || mbar_try_wait(bar, parity);
+        if (__all_sync(0xffffffffu, done)) return true;
+        const long long t0 = clock64(), limit = (long long)(lim * 2ull);
+#pragma unroll 1
+        while (true) {
+          if (!done) done = mbar_try_wait(bar, parity);
+          if (__all_sync(0xffffffffu, done)) return true;
+          if (__any_sync(0xffffffffu, clock64() - t0 > limit)) {
+            if (lane == 0) atomicOr(st, kStatusTimeout);
+            return false;
+          }
+        }
       };
       // Key tiles in order, over all units; for each query tile in turn its
-      // product, as its P comes in two parts, and right behind it the scores
-      // of the next key tile (of the next unit, too) into the same S: MMAs of
-      // one thread run in order.  Taking the query tiles in turn also keeps
-      // their softmaxes half a period apart, one with the other's products
-      // (with an issuer each they fell into step, and joint attention of
-      // 4608 tokens took 271 us instead of 217).
+      // product and right behind it the scores of the next key tile (of the
+      // next unit, too) into the same S: MMAs of one thread run in order.
+      // Taking the query tiles in turn also keeps their softmaxes half a
+      // period apart, one with the other's products.  This warp's own time
+      // between its MMAs is what the tensor core idles, so it polls
+      // together for what a step needs: lane 0 for V, 1 for K, 2 for P, 3 for the query tile, 4 for
+      // O to be free, 5 for V's masked rows.
       const uint64_t qd0 = sw128_kmajor_desc(smem_base);
       const uint64_t kd0 = sw128_kmajor_desc(ring), vd0 = sw128_mnmajor_desc(ring);
       constexpr uint32_t kSlot = C::kTile >> 4;  // in descriptor units
+      const uint32_t full0 = smem_u32(&kv_full[0]), empty0 = smem_u32(&kv_empty[0]);
+      const uint32_t own_bar = lane == 2 ? smem_u32(&p_full[0][0]) : lane == 3 ? smem_u32(&q_full[0]) : smem_u32(&o_free[0]);
       auto next_unit = [&](int u, Unit& x) {  // the first unit from u on with keys
         for (; u < units; u += ustep) {
           x = unit_of<MASK>(t, u);
@@ -437,70 +453,70 @@ __global__ void __launch_bounds__(kThreads, 1) attention_tile_kernel(const __gri
       };
       Unit y{};  // the unit of the tile whose scores are next
       int un = next_unit(u0, y), yj = 0;
-      bool more = un < units, last = false;  // last: the tile whose product is next is its unit's last
-      int nq = 0, j = 0, tile = 0;           // its query tiles (0: none yet), its place in the unit and among all
+      bool last = false;                       // the tile whose product is next is its unit's last
+      int nq = 0, nq_next = un < units ? y.nq : 0;  // query tiles of that tile (0: none), and of the next
+      int j = 0, tile = 0;                     // its place in the unit and among all
       int ks = 0, vs = 1 % S;
-      uint32_t kp = 0, vp = 0;               // phases of the ring
-      uint32_t pp = 0, qp = 0, op = 3;       // bit i: of p_full, q_full, o_free
-      while (ok && (more || nq > 0)) {
-        const int nq_next = more ? y.nq : 0;
+      uint32_t kp = 0, vp = 0;                 // phases of the ring
+      uint32_t pp = 0, qp = 0, op = 3;         // bit i: of p_full, q_full, o_free
+      while (nq | nq_next) {
         const bool last_next = yj == y.n - 1;
-        if (nq > 0) {
-          ok = wait(&kv_full[vs], vp);
-          if (MASK && ok) ok = wait(&v_ready[tile % kMaskSlots], (tile / kMaskSlots) & 1);
-        }
-        if (ok && more) ok = wait(&kv_full[ks], kp);
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-          const uint32_t ts = tm + i * kBN, to = tm + 256 + i * DP;
-          if (ok && i < nq) {
-            if (j == 0) {
-              ok = wait(&o_free[i], (op >> i) & 1);
-              op ^= 1u << i;
+          const bool mul = i < nq, score = i < nq_next;
+          {
+            uint32_t bar = own_bar + (lane == 2 ? 16 : 8) * i, parity = ((lane == 2 ? pp : lane == 3 ? qp : op) >> i) & 1;
+            bool need = lane == 2 ? mul : lane == 3 ? score && yj == 0 : lane == 4 ? mul && j == 0 : false;
+            if (i == 0 && lane < 2) {
+              bar = full0 + 8 * (lane == 0 ? vs : ks);
+              parity = lane == 0 ? vp : kp;
+              need = lane == 0 ? mul : score;
             }
-            const uint64_t vd = vd0 + uint32_t(vs) * kSlot;
-            if (ok) ok = wait(&p_full[i][0], (pp >> i) & 1);
-            if (ok) {
-              tc_fence_after();
-              mma_ts_4(to, ts, vd, C::kIdescO, j > 0);
-              mma_ts_2(to, ts + 32, vd + 512, C::kIdescO, 1);
-              ok = wait(&p_full[i][1], (pp >> i) & 1);
+            if (MASK && i == 0 && lane == 5) {
+              bar = smem_u32(&v_ready[tile % kMaskSlots]);
+              parity = (tile / kMaskSlots) & 1;
+              need = mul;
             }
-            pp ^= 1u << i;
-            if (ok) {
-              tc_fence_after();
-              mma_ts_2(to, ts + 48, vd + 768, C::kIdescO, 1);
-              if (last) mma_commit_elected(smem_u32(&o_done[i]));
-              if (i == nq - 1) mma_commit_elected(smem_u32(&kv_empty[vs]));
-            }
+            ok = wait_all(bar, parity, need);
           }
-          if (ok && i < nq_next) {
-            if (yj == 0) {
-              ok = wait(&q_full[i], (qp >> i) & 1);
-              qp ^= 1u << i;
-            }
-            if (ok) {
-              tc_fence_after();
-              const uint64_t qd = qd0 + uint32_t(i) * kSlot, kd = kd0 + uint32_t(ks) * kSlot;
-              mma_ss_panel(ts, qd, kd, C::kIdescS, 0);
-              if constexpr (C::kPanels == 2) mma_ss_panel(ts, qd + (kPanel >> 4), kd + (kPanel >> 4), C::kIdescS, 1);
-              mma_commit_elected(smem_u32(&s_full[i]));
-              if (last_next) mma_commit_elected(smem_u32(&q_empty[i]));
-              if (i == nq_next - 1) mma_commit_elected(smem_u32(&kv_empty[ks]));
-            }
+          if (!ok) break;
+          tc_fence_after();
+          const uint32_t ts = tm + i * kBN, to = tm + 256 + i * DP;
+          if (mul) {
+            const uint64_t vd = vd0 + uint32_t(vs) * kSlot;
+            mma_ts_4(to, ts, vd, C::kIdescO, j > 0);
+            mma_ts_2(to, ts + 32, vd + 512, C::kIdescO, 1);
+            ok = wait_all(smem_u32(&p_full[i][1]), (pp >> i) & 1, true);
+            if (!ok) break;
+            tc_fence_after();
+            mma_ts_2(to, ts + 48, vd + 768, C::kIdescO, 1);
+            if (last) mma_commit_elected(smem_u32(&o_done[i]));
+            if (i == nq - 1) mma_commit_elected(empty0 + 8 * vs);
+            pp ^= 1u << i;
+            if (j == 0) op ^= 1u << i;
+          }
+          if (score) {
+            const uint64_t qd = qd0 + uint32_t(i) * kSlot, kd = kd0 + uint32_t(ks) * kSlot;
+            mma_ss_panel(ts, qd, kd, C::kIdescS, 0);
+            if constexpr (C::kPanels == 2) mma_ss_panel(ts, qd + (kPanel >> 4), kd + (kPanel >> 4), C::kIdescS, 1);
+            mma_commit_elected(smem_u32(&s_full[i]));
+            if (last_next) mma_commit_elected(smem_u32(&q_empty[i]));
+            if (i == nq_next - 1) mma_commit_elected(empty0 + 8 * ks);
+            if (yj == 0) qp ^= 1u << i;
           }
         }
+        if (!ok) break;
         if (nq > 0) {
           vs += 2, vp ^= uint32_t(vs >= S), vs -= vs >= S ? S : 0;
           ++tile;
         }
         nq = nq_next, j = yj, last = last_next;
-        if (more) {
+        if (nq_next > 0) {
           ks += 2, kp ^= uint32_t(ks >= S), ks -= ks >= S ? S : 0;
           if (++yj == y.n) {
             yj = 0;
             un = next_unit(un + ustep, y);
-            more = un < units;
+            nq_next = un < units ? y.nq : 0;
           }
         }
       }
