@@ -146,11 +146,11 @@ cudaError_t launch_quantize_act_e4m3(const __nv_bfloat16* x, int M, int K, uint8
                                      cudaStream_t stream);
 cudaError_t launch_ternary_fp8(const Batch& batch, int pairs, cudaStream_t stream);
 
-// Rotary table: the frequency and axis of every channel pair.
+// Rotary table: the frequency of every channel pair and the pairs of every axis.
 constexpr int kRopeMaxPairs = 128;
 struct RopeFreqs {
   double turns[kRopeMaxPairs];  // theta^(-2 i / d_a), in quarter turns
-  uint8_t axis[kRopeMaxPairs];
+  int axis_pairs[4];
   int pairs, n_axes;
 };
 // cs [L][pairs][2] from ids [L][n_axes].

@@ -60,12 +60,14 @@ __global__ void __launch_bounds__(kTableThreads)
   pdl_trigger();
   const int P = f.pairs, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int m0 = int(blockIdx.x) * kTableRows, rows = min(kTableRows, L - m0);
-  double x[4];  // this lane's token
-#pragma unroll
-  for (int a = 0; a < 4; ++a) x[a] = a < f.n_axes && lane < rows ? double(ids[(long long)(m0 + lane) * f.n_axes + a]) : 0.0;
-  for (int j = warp; j < P; j += kTableThreads / 32) {
-    const int axis = f.axis[j];
-    tile[lane * (P + 1) + j] = cos_sin(axis == 0 ? x[0] : axis == 1 ? x[1] : axis == 2 ? x[2] : x[3], f.turns[j]);
+  float2* const row = tile + lane * (P + 1);
+  int end = 0;
+#pragma unroll 1
+  for (int a = 0; a < f.n_axes; ++a) {
+    const int begin = end;
+    end += f.axis_pairs[a];
+    const double x = lane < rows ? double(ids[(long long)(m0 + lane) * f.n_axes + a]) : 0.0;
+    for (int j = begin + warp; j < end; j += kTableThreads / 32) row[j] = cos_sin(x, f.turns[j]);
   }
   __syncthreads();
   float2* out = cs + (long long)m0 * P;

@@ -1008,8 +1008,9 @@ tern_status tern_rope_table(const float* ids, int64_t L, int n_axes, const int* 
                   2 * kRopeMaxPairs, a, d);
     for (int i = 0; i < d / 2; ++i) {
       f.turns[f.pairs] = std::pow(theta, -2.0 * i / d) * 0.63661977236758134308;  // 2 / pi
-      f.axis[f.pairs++] = uint8_t(a);
+      ++f.pairs;
     }
+    f.axis_pairs[a] = d / 2;
   }
   if (L == 0) return TERN_OK;
   if (!ids || !cs) return fail(TERN_ERR_INVALID_ARG, "null ids or cs");
