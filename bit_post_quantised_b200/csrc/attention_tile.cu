@@ -379,7 +379,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_tile_kernel(const __gri
       }
       const int row = x.q0 + i * kBM + (warp & 3) * 32 + lane;
       const float inv = sum == 0.f ? 0.f : 1.f / sum;
-      uint16_t* op = a.o + x.b * a.o_b + (long long)row * a.o_l + x.h * a.o_h;
+      uint16_t* op_row = a.o + x.b * a.o_b + (long long)row * a.o_l + x.h * a.o_h;
 #pragma unroll 1
       for (int c = 0; c < DP; c += 32) {
         uint32_t y[32];
@@ -396,15 +396,24 @@ __global__ void __launch_bounds__(kThreads, 1) attention_tile_kernel(const __gri
           if (lane == 0) mbar_arrive(smem_u32(&o_free[i]));
         }
         if (row < a.Lq) {
+          uint32_t z[16];
 #pragma unroll
-          for (int e = 0; e < 32; e += 8) {
-            if (c + e < a.D) {
-              uint32_t z[4];
+          for (int e = 0; e < 16; ++e) z[e] = pack2(__uint_as_float(y[2 * e]) * inv, __uint_as_float(y[2 * e + 1]) * inv);
+          // A thread's row is contiguous, its neighbours' rows are far: whole
+          // 32-byte sectors where o's alignment allows (a.D % 16 == 0 then).
+          if (t.o_sectors) {
 #pragma unroll
-              for (int k = 0; k < 4; ++k)
-                z[k] = pack2(__uint_as_float(y[e + 2 * k]) * inv, __uint_as_float(y[e + 2 * k + 1]) * inv);
-              *reinterpret_cast<uint4*>(op + c + e) = make_uint4(z[0], z[1], z[2], z[3]);
-            }
+            for (int e = 0; e < 16; e += 8)
+              if (c + 2 * e < a.D)
+                asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(op_row + c + 2 * e), "r"(z[e]),
+                             "r"(z[e + 1]), "r"(z[e + 2]), "r"(z[e + 3]), "r"(z[e + 4]), "r"(z[e + 5]), "r"(z[e + 6]),
+                             "r"(z[e + 7])
+                             : "memory");
+          } else {
+#pragma unroll
+            for (int e = 0; e < 16; e += 4)
+              if (c + 2 * e < a.D)
+                *reinterpret_cast<uint4*>(op_row + c + 2 * e) = make_uint4(z[e], z[e + 1], z[e + 2], z[e + 3]);
           }
         }
       }

@@ -30,6 +30,15 @@ namespace {
 constexpr int kTableThreads = 256;
 constexpr int kTableRows = 32;  // token rows per block, one per lane
 
+// sin(pi/2 f) / f and cos(pi/2 f): Taylor coefficients (pi/2)^k / k! with
+// alternating signs.  In constant memory they are operands of the 64-bit
+// multiply-adds; as literals each took two moves into registers per use.
+constexpr double kH = 1.57079632679489661923, kH2 = kH * kH, kH4 = kH2 * kH2, kH6 = kH4 * kH2, kH8 = kH4 * kH4,
+                 kH10 = kH6 * kH4, kH12 = kH6 * kH6;
+__constant__ double kSin[6] = {kH, -kH * kH2 / 6, kH * kH4 / 120, -kH * kH6 / 5040, kH * kH8 / 362880,
+                               -kH * kH10 / 39916800};
+__constant__ double kCos[7] = {1.0, -kH2 / 2, kH4 / 24, -kH6 / 720, kH8 / 40320, -kH10 / 3628800, kH12 / 479001600};
+
 // cos and sin of x * w quarter turns, each rounded once to fp32 (|x w| < 2^50).
 __device__ __forceinline__ float2 cos_sin(double x, double w) {
   // Adding 1.5 * 2^52 leaves the nearest integer n (its low bits count the
@@ -39,13 +48,8 @@ __device__ __forceinline__ float2 cos_sin(double x, double w) {
   const int q = __double2loint(u);
   const double f = fma(x, w, magic - u);
   const double z = f * f;
-  // sin(pi/2 f) / f and cos(pi/2 f): Taylor coefficients (pi/2)^k / k!, alternating.
-  constexpr double h = 1.57079632679489661923, h2 = h * h;
-  constexpr double s1 = h * h2 / 6, s2 = s1 * h2 / 20, s3 = s2 * h2 / 42, s4 = s3 * h2 / 72, s5 = s4 * h2 / 110;
-  constexpr double c1 = h2 / 2, c2 = c1 * h2 / 12, c3 = c2 * h2 / 30, c4 = c3 * h2 / 56, c5 = c4 * h2 / 90,
-                   c6 = c5 * h2 / 132;
-  const double s = f * fma(z, fma(z, fma(z, fma(z, fma(z, -s5, s4), -s3), s2), -s1), h);
-  const double c = fma(z, fma(z, fma(z, fma(z, fma(z, fma(z, c6, -c5), c4), -c3), c2), -c1), 1.0);
+  const double s = f * fma(z, fma(z, fma(z, fma(z, fma(z, kSin[5], kSin[4]), kSin[3]), kSin[2]), kSin[1]), kSin[0]);
+  const double c = fma(z, fma(z, fma(z, fma(z, fma(z, fma(z, kCos[6], kCos[5]), kCos[4]), kCos[3]), kCos[2]), kCos[1]), 1.0);
   const float fs = float(s), fc = float(c);
   const float cc = (q & 1) ? fs : fc, ss = (q & 1) ? fc : fs;
   // cos changes its sign for quarter turns 1 and 2, sin for 2 and 3.

@@ -1162,6 +1162,8 @@ tern_status tern_attention(const tern_attention_args* args, tern_stream_t stream
     ta.pairs = int(pairs);
     ta.units = int(tile_units);
     ta.ctas = ds->sms;
+    ta.o_sectors = aligned(t.o, 32) && t.D % 16 == 0 && (t.B <= 1 || t.o_b % 16 == 0) && (t.Lq <= 1 || t.o_l % 16 == 0) &&
+                   (t.H <= 1 || t.o_h % 16 == 0);
     ta.by_pairs = div_by(unsigned(pairs));
     ta.by_heads = div_by(unsigned(t.H));
     ta.by_group = div_by(unsigned(t.H / t.Hkv));

@@ -614,13 +614,19 @@ def gated_residual_norm(x: torch.Tensor, o: torch.Tensor, *, gate: Optional[torc
             if t.shape[0] != K:
                 raise ValueError(f"{name} must hold {K} values")
     raw = _launch_on((x, o, gate, scale, shift, post_weight, pre_weight, x_out, h), stream)
+    sxo = sh = (K, 1)
     if x_out is None:
         x_out = _empty_as(x, stream)
-    if h is None and (pre_norm != NORM_NONE or scale is not None or shift is not None):
+    else:
+        sxo = _bf16("x_out", x_out, (2,))
+        if x_out.shape != shape:
+            raise ValueError("x_out has x's shape")
+    if h is not None:
+        sh = _bf16("h", h, (2,))
+        if h.shape != shape:
+            raise ValueError("h has x's shape")
+    elif pre_norm != NORM_NONE or scale is not None or shift is not None:
         h = _empty_as(x, stream)
-    sxo, sh = _bf16("x_out", x_out, (2,)), (K, 1) if h is None else _bf16("h", h, (2,))
-    if x_out.shape != shape or (h is not None and h.shape != shape):
-        raise ValueError("x_out and h have x's shape")
     lds = (sx[0], so[0], sxo[0], sh[0]) if M > 1 else (K, K, K, K)
     p = lambda t: 0 if t is None else t.data_ptr()  # noqa: E731
     _check(lib().tern_gated_residual_norm(
