@@ -171,7 +171,7 @@ __global__ void __launch_bounds__(256) rope_kernel(const __grid_constant__ RopeA
 }  // namespace
 
 cudaError_t launch_rope_table(const float* ids, int L, const RopeFreqs& f, float* cs, cudaStream_t stream) {
-  const unsigned grid = unsigned((L + kTableRows - 1) / kTableRows);
+  const unsigned grid = (unsigned(L) + kTableRows - 1) / kTableRows;
   return launch_pdl(rope_table_kernel, dim3(grid), dim3(kTableThreads), kTableRows * (f.pairs + 1) * sizeof(float2), stream,
                     1, ids, L, f, reinterpret_cast<float2*>(cs));
 }

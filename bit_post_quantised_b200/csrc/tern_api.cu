@@ -1104,7 +1104,9 @@ tern_status tern_attention(const tern_attention_args* args, tern_stream_t stream
                 (long long)t.Hkv);
   if (t.Lq >= kMaxL || t.Lk >= kMaxL || t.B >= kMaxBH || t.H >= kMaxBH || t.B * t.H >= kMaxBH)
     return fail(TERN_ERR_UNSUPPORTED_SHAPE, "attention: Lq and Lk are below 2^30, B * H below 2^20");
-  if (!(t.scale > 0.f) || !std::isfinite(t.scale)) return fail(TERN_ERR_INVALID_ARG, "scale must be finite and > 0");
+  const float scale_log2 = t.scale * 1.44269504088896340736f;
+  if (!(t.scale > 0.f) || !std::isfinite(scale_log2))
+    return fail(TERN_ERR_INVALID_ARG, "scale must be > 0 and below 2^127 (scale=%g)", double(t.scale));
   if (!t.q || !t.o || (t.Lk > 0 && (!t.k || !t.v))) return fail(TERN_ERR_INVALID_ARG, "null q, k, v or o");
   if (!aligned(t.q, 16) || !aligned(t.o, 16) || (t.Lk > 0 && (!aligned(t.k, 16) || !aligned(t.v, 16))))
     return fail(TERN_ERR_MISALIGNED, "q, k, v and o need 16-byte alignment");
@@ -1129,7 +1131,7 @@ tern_status tern_attention(const tern_attention_args* args, tern_stream_t stream
   a.key_mask = t.key_mask;
   a.mask_ld = t.mask_ld;
   a.B = int(t.B), a.Lq = int(t.Lq), a.Lk = int(t.Lk), a.H = int(t.H), a.Hkv = int(t.Hkv), a.D = int(t.D);
-  a.scale_log2 = t.scale * 1.44269504088896340736f;
+  a.scale_log2 = scale_log2;
   if ((t.Lq * (t.H / t.Hkv) + 15) / 16 * t.Hkv * t.B * 16 > INT32_MAX)
     return fail(TERN_ERR_UNSUPPORTED_SHAPE, "attention: too many query rows");
   int dev;

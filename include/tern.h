@@ -429,7 +429,7 @@ TERN_API tern_status tern_rope(const tern_rope_tensor* tensors, int count, int64
  * (TERN_ERR_UNSUPPORTED_SHAPE); pointers 16-byte aligned, strides multiples
  * of 8 below 2^38, 0 allowed in q, k and v (a broadcast); the elements of o
  * are distinct (strides as tern_rope's y) and o overlaps no input.  scale > 0
- * and finite.  B, Lq or H == 0 is a no-op; Lk == 0 writes zeros (k and v may
+ * and below 2^127.  B, Lq or H == 0 is a no-op; Lk == 0 writes zeros (k and v may
  * be NULL).
  */
 typedef struct {

@@ -140,7 +140,7 @@ def test_attention_rejects(L):
     assert _attn(L, Hkv=3) == SHAPE and _attn(L, Hkv=0) == SHAPE
     assert _attn(L, Lq=1 << 30) == SHAPE and _attn(L, Lk=1 << 30) == SHAPE
     assert _attn(L, B=1 << 19) == SHAPE and _attn(L, H=1 << 21, Hkv=1) == SHAPE
-    for s in (0.0, -1.0, float("nan"), float("inf")):
+    for s in (0.0, -1.0, float("nan"), float("inf"), 3e38):
         assert _attn(L, scale=s) == INVALID
     for n in "qkvo":
         assert _attn(L, **{n: 0}) == INVALID and _attn(L, **{n: F + 0x5000008}) == MISALIGNED, n
