@@ -194,8 +194,9 @@ def _empty(*shape, dtype, device, stream=None) -> torch.Tensor:
 
 def _empty_as(t: torch.Tensor, stream=None) -> torch.Tensor:
     """A contiguous output buffer of t's shape and type (see _empty)."""
-    return torch.empty_like(t) if stream is None and t.is_contiguous() else _empty(t.shape, dtype=t.dtype,
-                                                                                   device=t.device, stream=stream)
+    if stream is None:
+        return torch.empty_like(t, memory_format=torch.contiguous_format)
+    return _empty(t.shape, dtype=t.dtype, device=t.device, stream=stream)
 
 
 def packed_bytes(N: int, K: int) -> int:
@@ -499,12 +500,14 @@ def rope(xs: Sequence[torch.Tensor], cs: torch.Tensor, halves: bool = False,
     if not xs:
         return []
     shape = xs[0].shape
-    strides = []
+    nd = len(shape)
+    parts = []  # (address, heads, strides) of each
     for x in xs:
-        strides.append(_bf16("x", x, (3, 4)))
+        st = _bf16("x", x, (nd,) if nd == 3 or nd == 4 else (3, 4))
         sh = x.shape
-        if len(sh) != len(shape) or sh[:-2] != shape[:-2] or sh[-1] != shape[-1]:
+        if sh[0] != shape[0] or sh[-1] != shape[-1] or (nd == 4 and sh[1] != shape[1]):
             raise ValueError("the tensors must share their tokens and head size")
+        parts.append((x.data_ptr(), sh[-2], st if nd == 4 else (0, *st)))
     table = cs.shape
     if cs.dtype is not torch.float32 or len(table) != 3 or table[2] != 2 or not cs.is_contiguous():
         raise ValueError("cs must be contiguous fp32 [rows, P, 2]")
@@ -514,14 +517,14 @@ def rope(xs: Sequence[torch.Tensor], cs: torch.Tensor, halves: bool = False,
     elif len(outs) != len(xs):
         raise ValueError("one output per tensor")
     args = []
-    for x, y, sx in zip(xs, outs, strides):
-        if y.shape != x.shape:
-            raise ValueError("an output has its input's shape")
-        sy = _bf16("out", y, (3, 4))
-        if len(sx) == 3:
-            sx, sy = (0, *sx), (0, *sy)
-        args += (x.data_ptr(), y.data_ptr(), x.shape[-2], *sx[:3], *sy[:3])
-    B, L = (shape[0], shape[1]) if len(shape) == 4 else (1, shape[0])
+    for x, y, (at, heads, sx) in zip(xs, outs, parts):
+        sy = y.stride()
+        if y.shape != x.shape or y.dtype is not torch.bfloat16 or (sy[-1] != 1 and shape[-1] > 1):
+            raise ValueError("an output is bf16 of its input's shape with adjacent channels")
+        if nd == 3:
+            sy = (0, *sy)
+        args += (at, y.data_ptr(), heads, sx[0], sx[1], sx[2], sy[0], sy[1], sy[2])
+    B, L = (shape[0], shape[1]) if nd == 4 else (1, shape[0])
     _check(lib().tern_rope(struct.pack("2P7q" * len(xs), *args), len(xs), B, L, shape[-1], cs.data_ptr(), table[0],
                            table[1], 1 if halves else 0, raw))
     return list(outs)
