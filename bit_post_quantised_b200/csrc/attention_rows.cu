@@ -28,9 +28,9 @@
 //
 // The ring is sized for two CTAs an SM, which also lets eight clusters of 16
 // be resident.  Long caches of few heads are bound by the instructions of a
-// block's chain (16,384 keys x 8 heads: 29.8 us, 2.3 TB/s; blocks of 32 keys,
+// block's chain (16,384 keys x 8 heads: 21.5 us, 3.1 TB/s; blocks of 32 keys,
 // one CTA an SM, leave room for seven clusters only: 46 us), short calls by
-// their latency (512 keys x 24 heads, one query: 7.3 us).
+// their latency (512 keys x 24 heads, one query: 6.8 us).
 //
 // Join: the four warps of a CTA combine their (max, sum, output) through
 // shared memory, then the CTAs of the cluster through distributed shared
@@ -151,17 +151,33 @@ __global__ void __launch_bounds__(kWarps * 32, 2) attention_rows_kernel(const __
   const int blocks = (len + kKeys - 1) / kKeys;
   const int stride = splits * kWarps;
   const uint32_t ring = smem_u32(dyn) + uint32_t(warp * ST * 2 * M::kBlock);
-  // The keys and values of block `blk` into ring stage `stage`.
+  // The keys and values of block `blk` into ring stage `stage`.  A lane copies
+  // group `lane % kChunks` of every kStep-th key; the swizzle of K is the
+  // lane's own then, that of V one of four.
+  constexpr int kStep = 32 / kChunks;
+  const int r0 = lane / kChunks, c0 = lane % kChunks;
+  const bool in_head = 8 * c0 < a.D;
+  const uint32_t k_at = uint32_t(r0 * DP * 2) + 16 * (c0 ^ ((r0 & 1) << 2));
+  uint32_t v_at[8 / kStep];
+#pragma unroll
+  for (int n = 0; n < 8 / kStep; ++n) {
+    const int r = r0 + n * kStep;
+    v_at[n] = uint32_t(M::kBlock + r * DP * 2) + 16 * (c0 ^ (r & 6));
+  }
   auto fetch = [&](int blk, int stage) {
     const uint32_t base = ring + uint32_t(stage * 2 * M::kBlock);
+    const int key0 = blk * kKeys + r0;
+    const uint16_t* kr = kp + (long long)key0 * a.k_l + 8 * c0;
+    const uint16_t* vr = vp + (long long)key0 * a.v_l + 8 * c0;
+    const long long k_step = kStep * a.k_l, v_step = kStep * a.v_l;
 #pragma unroll
-    for (int n = 0; n < kKeys * kChunks / 32; ++n) {
-      const int at = n * 32 + lane, r = at / kChunks, c = at % kChunks;
-      const int key = blk * kKeys + r;
-      const bool ok = key < len && 8 * c < a.D;
-      const uint32_t row = base + uint32_t(r * DP * 2);
-      copy16(row + 16 * (c ^ ((r & 1) << 2)), ok ? kp + (long long)key * a.k_l + 8 * c : kp, ok);
-      copy16(row + M::kBlock + 16 * (c ^ (r & 6)), ok ? vp + (long long)key * a.v_l + 8 * c : vp, ok);
+    for (int n = 0; n < kKeys / kStep; ++n) {
+      static_assert(8 % kStep == 0 && kStep % 2 == 0, "the swizzles repeat every eight keys");
+      const bool ok = in_head && key0 + n * kStep < len;
+      copy16(base + k_at + n * (kStep * DP * 2), ok ? kr : kp, ok);
+      copy16(base + v_at[n % (8 / kStep)] + n / (8 / kStep) * (8 * DP * 2), ok ? vr : vp, ok);
+      kr += k_step;
+      vr += v_step;
     }
   };
   const int first = split * kWarps + warp;
@@ -173,14 +189,17 @@ __global__ void __launch_bounds__(kWarps * 32, 2) attention_rows_kernel(const __
   int stage = 0;
   for (int blk = first; blk < blocks; blk += stride) {
     // Keys of this thread: its score columns and its value rows are the same.
-    bool ok[2][2];
+    const bool whole = !mask && (blk + 1) * kKeys <= len;
+    bool ok[2][2] = {{true, true}, {true, true}};
+    if (!whole) {
 #pragma unroll
-    for (int nt = 0; nt < 2; ++nt)
+      for (int nt = 0; nt < 2; ++nt)
 #pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        const int key = blk * kKeys + nt * 8 + 2 * t + e;
-        ok[nt][e] = key < len && (!mask || mask[key]);
-      }
+        for (int e = 0; e < 2; ++e) {
+          const int key = blk * kKeys + nt * 8 + 2 * t + e;
+          ok[nt][e] = key < len && (!mask || mask[key]);
+        }
+    }
     asm volatile("cp.async.wait_group %0;" ::"n"(ST - 2) : "memory");
     __syncwarp();  // every lane's copies are in, and its reads of the stage refilled next are done
     if (blk + (ST - 1) * stride < blocks) fetch(blk + (ST - 1) * stride, stage == 0 ? ST - 1 : stage - 1);
@@ -198,19 +217,20 @@ __global__ void __launch_bounds__(kWarps * 32, 2) attention_rows_kernel(const __
         mma_16816(s[nt], q[2 * i][0], q[2 * i][1], q[2 * i][2], q[2 * i][3], k4.x, k4.y);
         mma_16816(s[nt], q[2 * i + 1][0], q[2 * i + 1][1], q[2 * i + 1][2], q[2 * i + 1][3], k4.z, k4.w);
       }
-    float top[2];
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      top[h] = -INFINITY;
+    for (int nt = 0; nt < 2; ++nt)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) s[nt][e] *= a.scale_log2;
+    if (!whole) {
 #pragma unroll
       for (int nt = 0; nt < 2; ++nt)
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          float& v = s[nt][2 * h + e];
-          v = ok[nt][e] ? v * a.scale_log2 : -INFINITY;
-          top[h] = fmaxf(top[h], v);
-        }
+        for (int e = 0; e < 4; ++e)
+          if (!ok[nt][e & 1]) s[nt][e] = -INFINITY;
     }
+    float top[2];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) top[h] = fmaxf(fmaxf(s[0][2 * h], s[0][2 * h + 1]), fmaxf(s[1][2 * h], s[1][2 * h + 1]));
 #pragma unroll
     for (int x = 1; x <= 2; x *= 2)
 #pragma unroll
@@ -244,7 +264,11 @@ __global__ void __launch_bounds__(kWarps * 32, 2) attention_rows_kernel(const __
       for (int e = 0; e < 4; ++e) {
         const int r = 2 * t + (e & 1) + (e >> 1) * 8;
         vv[e] = lds16(vb + uint32_t(r * DP * 2) + 16 * ((8 * c + g) ^ (r & 6)));
-        if (!ok[e >> 1][e & 1]) vv[e] = make_uint4(0u, 0u, 0u, 0u);
+      }
+      if (!whole) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          if (!ok[e >> 1][e & 1]) vv[e] = make_uint4(0u, 0u, 0u, 0u);
       }
       const uint32_t* w0 = &vv[0].x;
       const uint32_t* w1 = &vv[1].x;
