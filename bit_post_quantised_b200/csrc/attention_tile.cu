@@ -8,16 +8,19 @@
 // V tiles stream through one ring (TMA, 128-byte swizzle).  CTAs are
 // persistent, one per SM, and every role runs ahead into its next unit: with
 // few keys the loads and the output of one unit hide behind the products of
-// another (4096 x 512 x 24 heads: 45 us as one CTA per unit).  Per key
+// another (4096 x 512 x 24 heads: 30 us, 45 us as one CTA per unit).  Per key
 // tile and query tile: S = Q K^T into 128 TMEM columns; four softmax warps
 // read S (a thread owns a row), write P as bf16 over the first half of S;
 // O += P V with P from TMEM and V as stored (rows of keys: the MN-major form of
 // the B operand), O staying in TMEM over all keys.  While one query tile's
 // softmax runs, the other's products do.
 //
-//   warps 0-3, 4-7  softmax and output of query tile 0 / 1
+//   warps 0-3, 4-7  softmax of query tile 0 / 1
 //   warp 8          issues the MMAs        warp 9   TMA
 //   warp 10         validity of the keys (masked launches)
+//   warps 12-15     output of both query tiles, while the softmax warps are
+//                   in the next unit already (written by those themselves:
+//                   4096 x 512 +5%, 4096 x 77 +10%)
 //
 // The reference m only follows the running maximum when that has grown by
 // more than 8 in log2 units: until then probabilities are at most 2^8, which
@@ -31,14 +34,17 @@
 // tensor core needs 2048 cycles and their 32,768 exponentials, at 16 a cycle,
 // as many.  Measured, a query tile's chain is its softmax (scores 100, maximum
 // 300, exponentials 1450 of at least 1024, barriers) and then the product and
-// the next scores (1024 and their latencies): a period of 3340 cycles, with
-// the two query tiles half a period apart, 0.73 of the measured cuBLAS rate on
-// 4608 x 4608 x 24 heads (210 us).  Tried and slower: part of the exponentials
-// as polynomials on the FMA pipe (the softmax is bound by its dependent
-// issue, not by the exponentials' pipe alone: +3 to +9%), 64-key steps with two
-// score buffers a query tile (scores of 64 keys read Q from shared memory at
-// half the rate the tensor core needs: +4 to +18%), an issuing warp per query
-// tile (the softmaxes fall into step: +29%; in turns: -1.5%, others +3%).
+// the next scores (1024 and their latencies): a period of some 3300 cycles,
+// with the two query tiles half a period apart; 4608 x 4608 x 24 heads take
+// 198 us, 0.77 of the measured cuBLAS rate.  Tried and slower: part of the
+// exponentials as polynomials on the FMA pipe (the softmax is bound by its
+// dependent issue, not by the exponentials' pipe alone: +3 to +9%), 64-key
+// steps with two score buffers a query tile (scores of 64 keys read Q from
+// shared memory at 48 cycles per 32-cycle MMA: +4 to +18%), an issuing warp per
+// query tile (the softmaxes fall into step: +29%; taking turns: -1.5% there,
+// +3% elsewhere), two threads a row (+4%), the search for the maximum between
+// exponentials that start from the old one (+4%), the last quarter's
+// exponentials in the output warps (+6%).
 //
 // Masked keys: S is replaced by -inf there (whatever it holds) and their V
 // rows are overwritten with zeros in shared memory, since 0 * NaN would reach
@@ -56,10 +62,11 @@ constexpr int kBM = 128;        // query rows per tile, two tiles a CTA
 constexpr int kBN = 128;        // keys per K or V tile in shared memory
 constexpr int kFirst = 96;      // keys of a tile whose P is handed over first
 constexpr int kPanel = 16384;   // 128 rows x 64 channels of bf16
-constexpr int kThreads = 384;
-constexpr int kSoftmaxRegs = 208, kOtherRegs = 80;
-// What the register split asks for has to be there at launch (__launch_bounds__ gives 168 a thread).
-static_assert(256 * kSoftmaxRegs + 128 * kOtherRegs <= kThreads * 168, "register split");
+constexpr int kThreads = 512;
+constexpr int kSoftmaxRegs = 192, kOtherRegs = 72, kOutRegs = 56;
+// What the register split asks for has to be there at launch (__launch_bounds__ gives 128 a thread).
+constexpr int kLaunchRegs = 128;
+static_assert(256 * kSoftmaxRegs + 128 * kOtherRegs + 128 * kOutRegs <= kThreads * kLaunchRegs, "register split");
 
 template <int DP>
 struct TileShape {
@@ -211,6 +218,8 @@ __global__ void __launch_bounds__(kThreads, 1) attention_tile_kernel(const __gri
   __shared__ __align__(8) uint64_t p_full[2][2];   // P of the first keys is there (and O rescaled); of the rest
   __shared__ __align__(8) uint64_t o_done[2];      // the unit's O is complete
   __shared__ __align__(8) uint64_t o_free[2];      // the unit's O has been read
+  __shared__ __align__(8) uint64_t sum_full[2];    // 1 / sum of the unit's rows
+  __shared__ float inv_sum[2][kBM];
   __shared__ __align__(8) uint64_t drain_bar;      // every MMA issued is done
   __shared__ __align__(8) uint64_t v_ready[MASK ? kMaskSlots : 1];   // masked rows of a tile's V are zero
   __shared__ __align__(8) uint64_t m_full[MASK ? kMaskSlots : 1];    // validity of a key tile written
@@ -236,6 +245,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_tile_kernel(const __gri
       mbar_init(smem_u32(&p_full[i][1]), 4);
       mbar_init(smem_u32(&o_done[i]), 1);
       mbar_init(smem_u32(&o_free[i]), 4);
+      mbar_init(smem_u32(&sum_full[i]), 4);
     }
     for (int s = 0; s < S; ++s) {
       mbar_init(smem_u32(&kv_full[s]), 1);
@@ -263,14 +273,14 @@ __global__ void __launch_bounds__(kThreads, 1) attention_tile_kernel(const __gri
   const uint32_t tmem = tmem_base_sh;
 
   if (warp < 8) {
-    // ------------------------------------------------------ softmax, output
+    // ------------------------------------------------------ softmax
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs));
     const int i = warp >> 2;  // query tile
     const uint32_t lane_off = uint32_t((warp & 3) * 32) << 16;
     const uint32_t ts = tmem + lane_off + i * kBN, to = tmem + lane_off + 256 + i * DP;
     const float sl = a.scale_log2;
     const float2 sl2 = make_float2(sl, sl);
-    uint32_t sp = 0, op = 0;  // phases of s_full and o_done
+    uint32_t sp = 0, fp = 1;  // phases of s_full and o_free
     int mt = 0;  // key tiles so far (the slot and phase of the validity words)
     bool ok = true;
     for (int u = u0; u < units && ok; u += ustep) {
@@ -371,49 +381,73 @@ __global__ void __launch_bounds__(kThreads, 1) attention_tile_kernel(const __gri
         sum += acc[0].x + acc[0].y;
       }
       if (!ok) break;
-      if (x.n > 0) {
-        ok = __all_sync(0xffffffffu, bar_wait(smem_u32(&o_done[i]), op, lim, st));
-        if (!ok) break;
-        op ^= 1;
-        tc_fence_after();
-      }
-      const int row = x.q0 + i * kBM + (warp & 3) * 32 + lane;
-      const float inv = sum == 0.f ? 0.f : 1.f / sum;
-      uint16_t* op_row = a.o + x.b * a.o_b + (long long)row * a.o_l + x.h * a.o_h;
+      if (x.n == 0) continue;
+      // The rows' sums to the output warps, once they are through with the unit before.
+      ok = __all_sync(0xffffffffu, bar_wait(smem_u32(&o_free[i]), fp, lim, st));
+      if (!ok) break;
+      fp ^= 1;
+      inv_sum[i][(warp & 3) * 32 + lane] = sum == 0.f ? 0.f : 1.f / sum;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_u32(&sum_full[i]));
+    }
+  } else if (warp >= 12) {
+    // ------------------------------------------------------ output
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOutRegs));
+    const int r = (warp & 3) * 32 + lane;
+    const uint32_t lane_off = uint32_t((warp & 3) * 32) << 16;
+    uint32_t ph = 0;  // bit i: phase of o_done and sum_full
+    bool ok = true;
+    for (int u = u0; u < units && ok; u += ustep) {
+      const Unit x = unit_of<MASK>(t, u);
 #pragma unroll 1
-      for (int c = 0; c < DP; c += 32) {
-        uint32_t y[32];
+      for (int i = 0; i < x.nq; ++i) {
+        const uint32_t to = tmem + lane_off + 256 + i * DP;
+        float inv = 0.f;
         if (x.n > 0) {
-          tmem_ld32(to + c, y);
-          tmem_wait_ld();
-        } else {
-#pragma unroll
-          for (int e = 0; e < 32; ++e) y[e] = 0u;
+          ok = __all_sync(0xffffffffu, bar_wait(smem_u32(&sum_full[i]), (ph >> i) & 1, lim, st) &&
+                                           bar_wait(smem_u32(&o_done[i]), (ph >> i) & 1, lim, st));
+          if (!ok) break;
+          ph ^= 1u << i;
+          tc_fence_after();
+          inv = inv_sum[i][r];
         }
-        if (x.n > 0 && c + 32 == DP) {
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(smem_u32(&o_free[i]));
-        }
-        if (row < a.Lq) {
-          uint32_t z[16];
-#pragma unroll
-          for (int e = 0; e < 16; ++e) z[e] = pack2(__uint_as_float(y[2 * e]) * inv, __uint_as_float(y[2 * e + 1]) * inv);
-          // A thread's row is contiguous, its neighbours' rows are far: whole
-          // 32-byte sectors where o's alignment allows (a.D % 16 == 0 then).
-          if (t.o_sectors) {
-#pragma unroll
-            for (int e = 0; e < 16; e += 8)
-              if (c + 2 * e < a.D)
-                asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(op_row + c + 2 * e), "r"(z[e]),
-                             "r"(z[e + 1]), "r"(z[e + 2]), "r"(z[e + 3]), "r"(z[e + 4]), "r"(z[e + 5]), "r"(z[e + 6]),
-                             "r"(z[e + 7])
-                             : "memory");
+        const int row = x.q0 + i * kBM + r;
+        uint16_t* o_row = a.o + x.b * a.o_b + (long long)row * a.o_l + x.h * a.o_h;
+#pragma unroll 1
+        for (int c = 0; c < DP; c += 32) {
+          uint32_t y[32];
+          if (x.n > 0) {
+            tmem_ld32(to + c, y);
+            tmem_wait_ld();
           } else {
 #pragma unroll
-            for (int e = 0; e < 16; e += 4)
-              if (c + 2 * e < a.D)
-                *reinterpret_cast<uint4*>(op_row + c + 2 * e) = make_uint4(z[e], z[e + 1], z[e + 2], z[e + 3]);
+            for (int e = 0; e < 32; ++e) y[e] = 0u;
+          }
+          if (x.n > 0 && c + 32 == DP) {
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(smem_u32(&o_free[i]));
+          }
+          if (row < a.Lq) {
+            uint32_t z[16];
+#pragma unroll
+            for (int e = 0; e < 16; ++e) z[e] = pack2(__uint_as_float(y[2 * e]) * inv, __uint_as_float(y[2 * e + 1]) * inv);
+            // A thread's row is contiguous, its neighbours' rows are far: whole
+            // 32-byte sectors where o's alignment allows (a.D % 16 == 0 then).
+            if (t.o_sectors) {
+#pragma unroll
+              for (int e = 0; e < 16; e += 8)
+                if (c + 2 * e < a.D)
+                  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(o_row + c + 2 * e), "r"(z[e]),
+                               "r"(z[e + 1]), "r"(z[e + 2]), "r"(z[e + 3]), "r"(z[e + 4]), "r"(z[e + 5]), "r"(z[e + 6]),
+                               "r"(z[e + 7])
+                               : "memory");
+            } else {
+#pragma unroll
+              for (int e = 0; e < 16; e += 4)
+                if (c + 2 * e < a.D)
+                  *reinterpret_cast<uint4*>(o_row + c + 2 * e) = make_uint4(z[e], z[e + 1], z[e + 2], z[e + 3]);
+            }
           }
         }
       }
@@ -638,7 +672,7 @@ cudaError_t launch_one(const AttnTileArgs& t, cudaStream_t stream) {
   if (ready_dev != dev) {
     cudaFuncAttributes f;
     if ((e = cudaFuncGetAttributes(&f, attention_tile_kernel<DP, MASK>)) != cudaSuccess) return e;
-    if (f.numRegs * kThreads < 256 * kSoftmaxRegs + 128 * kOtherRegs) return cudaErrorInvalidConfiguration;
+    if (f.numRegs * kThreads < 256 * kSoftmaxRegs + 128 * kOtherRegs + 128 * kOutRegs) return cudaErrorInvalidConfiguration;
     e = cudaFuncSetAttribute(attention_tile_kernel<DP, MASK>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
     if (e != cudaSuccess) return e;
     ready_dev = dev;
