@@ -385,12 +385,17 @@ cudaError_t launch_ni(const AttnArgs& a, int splits, cudaStream_t stream) {
 
 }  // namespace
 
+int attention_rows_splits(long long units, long long Lk, int sms) {
+  // While the CTAs fit the GPU at once (two an SM) and each warp keeps a block.
+  int splits = 1;
+  while (splits < 16 && units * splits * 2 <= 2 * sms && splits * 2 * kWarps <= (Lk + kKeys - 1) / kKeys) splits *= 2;
+  return splits;
+}
+
 cudaError_t launch_attention_rows(const AttnArgs& a, int sms, cudaStream_t stream) {
   const long long rows = (long long)a.Lq * (a.H / a.Hkv);
   const long long units = (rows + kRows - 1) / kRows * a.Hkv * a.B;
-  // Split the keys while the CTAs fit the GPU at once (two an SM) and each warp keeps a block.
-  int splits = 1;
-  while (splits < 16 && units * splits * 2 <= 2 * sms && splits * 2 * kWarps <= (a.Lk + kKeys - 1) / kKeys) splits *= 2;
+  const int splits = attention_rows_splits(units, a.Lk, sms);
   switch ((a.D + 31) / 32) {
     case 1: return launch_ni<1>(a, splits, stream);
     case 2: return launch_ni<2>(a, splits, stream);

@@ -1138,18 +1138,26 @@ tern_status tern_attention(const tern_attention_args* args, tern_stream_t stream
   DeviceState* ds;
   tern_status s;
   if ((s = current_device(&dev, &ds)) != TERN_OK) return s;
-  // The row kernel's time grows with its 16-row units times the keys, some 7000
-  // of them a microsecond, behind a shorter start; the tile kernel's with its
-  // rounds over the SMs times the key tiles, 1.4 us each, however few of a
-  // tile's rows there are.  Measured (us, rows | tiles): 1531 keys, 60 units
-  // 10 | 19; 4096 keys, 48 units 32 | 50, 96 units 58 | 50; 512 keys, 24 units
-  // 8.2 | 9.4, 96 units 14 | 9.5; 256 keys, 64 units 5.9 | 7.2.  (A tensor map has
-  // no dimension of stride 0: tokens that are one broadcast row take rows.)
+  // Each kernel's time as it was measured, in us.  Rows: a start, and for every
+  // wave of its CTAs (two an SM) the 16-key blocks that a warp takes one after
+  // the other; tiles: a start, and for every round of units over the SMs its
+  // key tiles, however few of a tile's rows there are.  Measured (us, rows |
+  // tiles): 24 heads of 128, 512 keys: 32 queries 8.4 | 9.1, 64 queries 11.4 |
+  // 9.1; 4096 keys: 32 queries 23 | 50, 96 queries 39 | 50; 64 x 1 query of 8 heads, 4096
+  // keys 154 | 193; 4 heads of 64, 256 x 256 5.3 | 6.9; 24 heads of 64, 256 x 77
+  // 9.8 | 5.7.  (A tensor map has no dimension of stride 0: tokens that are one
+  // broadcast row take rows.)
   const bool flat = (t.Lq > 1 && t.q_l == 0) || (t.Lk > 1 && (t.k_l == 0 || t.v_l == 0));
   const int64_t pairs = (t.Lq + 255) / 256, tile_units = pairs * t.B * t.H;
   const int64_t row_units = (t.Lq * (t.H / t.Hkv) + 15) / 16 * t.Hkv * t.B;
   const int64_t rounds = (tile_units + ds->sms - 1) / ds->sms;
-  const bool rows = row_units * t.Lk <= 7000 + ds->sms / 2 * ((t.Lk + 127) / 128 * 128) * rounds;
+  const int splits = attention_rows_splits(row_units, t.Lk, ds->sms);
+  const int64_t waves = (row_units * splits + 2 * ds->sms - 1) / (2 * ds->sms);
+  const int64_t blocks = (t.Lk + 64 * splits - 1) / (64 * splits), tiles = (t.Lk + 127) / 128;
+  const bool wide = t.D > 64;
+  const double rows_us = 2.5 + (splits > 1 ? 1. : 0.) + double(waves) * (wide ? 2.5 + 1.05 * blocks : 1.2 + 0.65 * blocks);
+  const double tiles_us = (wide ? 3.3 : 4.9) + (wide ? 1.47 : 0.98) * double(rounds) * double(tiles);
+  const bool rows = rows_us <= tiles_us;
   cudaError_t e;
   if (rows || flat || t.Lk == 0) {
     e = launch_attention_rows(a, ds->sms, reinterpret_cast<cudaStream_t>(stream));
