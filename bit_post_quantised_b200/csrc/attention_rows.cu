@@ -27,10 +27,12 @@
 // without a valid key gives zeros.
 //
 // The ring is sized for two CTAs an SM, which also lets eight clusters of 16
-// be resident.  Long caches of few heads are bound by the instructions of a
-// block's chain (16,384 keys x 8 heads: 21.5 us, 3.1 TB/s; blocks of 32 keys,
-// one CTA an SM, leave room for seven clusters only: 46 us), short calls by
-// their latency (512 keys x 24 heads, one query: 6.8 us).
+// be resident.  Many heads are bound by memory (64 x 1 query, 4096 keys, 8 heads:
+// 153 us, 7.0 TB/s); few of them by a block's chain in its warp and the loads'
+// latency alike (16,384 keys x 8 heads: 21.1 us, 3.2 TB/s; 17 with the copies
+// alone, 17.4 without them; blocks of 32 keys, one CTA an SM, leave room for
+// seven clusters only: 46 us), short calls by their latency (512 keys x 24 heads,
+// one query: 6.8 us, of which the copies and the join are 5.6).
 //
 // Join: the four warps of a CTA combine their (max, sum, output) through
 // shared memory, then the CTAs of the cluster through distributed shared
@@ -49,8 +51,7 @@ constexpr int kKeys = 16;  // of a block
 
 __device__ __forceinline__ void mma_16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                           uint32_t b1) {
-  asm volatile(
-      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
@@ -206,21 +207,29 @@ __global__ void __launch_bounds__(kWarps * 32, 2) attention_rows_kernel(const __
     asm volatile("cp.async.commit_group;" ::: "memory");
     const uint32_t kb = ring + uint32_t(stage * 2 * M::kBlock), vb = kb + M::kBlock;
     stage = stage == ST - 1 ? 0 : stage + 1;
-    float s[2][4];
-#pragma unroll
-    for (int nt = 0; nt < 2; ++nt) s[nt][0] = s[nt][1] = s[nt][2] = s[nt][3] = 0.f;
-#pragma unroll
-    for (int i = 0; i < NI; ++i)
-#pragma unroll
-      for (int nt = 0; nt < 2; ++nt) {
-        const uint4 k4 = lds16(kb + uint32_t((nt * 8 + g) * DP * 2) + 16 * ((4 * i + t) ^ ((g & 1) << 2)));
-        mma_16816(s[nt], q[2 * i][0], q[2 * i][1], q[2 * i][2], q[2 * i][3], k4.x, k4.y);
-        mma_16816(s[nt], q[2 * i + 1][0], q[2 * i + 1][1], q[2 * i + 1][2], q[2 * i + 1][3], k4.z, k4.w);
-      }
+    // Two sums a tile, so that four products are in flight.
+    float s[2][4], s2[2][4];
 #pragma unroll
     for (int nt = 0; nt < 2; ++nt)
 #pragma unroll
-      for (int e = 0; e < 4; ++e) s[nt][e] *= a.scale_log2;
+      for (int e = 0; e < 4; ++e) s[nt][e] = s2[nt][e] = 0.f;
+#pragma unroll
+    for (int i = 0; i < NI; ++i) {
+      uint4 k4[2];
+#pragma unroll
+      for (int nt = 0; nt < 2; ++nt)
+        k4[nt] = lds16(kb + uint32_t((nt * 8 + g) * DP * 2) + 16 * ((4 * i + t) ^ ((g & 1) << 2)));
+#pragma unroll
+      for (int nt = 0; nt < 2; ++nt)
+        mma_16816(s[nt], q[2 * i][0], q[2 * i][1], q[2 * i][2], q[2 * i][3], k4[nt].x, k4[nt].y);
+#pragma unroll
+      for (int nt = 0; nt < 2; ++nt)
+        mma_16816(s2[nt], q[2 * i + 1][0], q[2 * i + 1][1], q[2 * i + 1][2], q[2 * i + 1][3], k4[nt].z, k4[nt].w);
+    }
+#pragma unroll
+    for (int nt = 0; nt < 2; ++nt)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) s[nt][e] = (s[nt][e] + s2[nt][e]) * a.scale_log2;
     if (!whole) {
 #pragma unroll
       for (int nt = 0; nt < 2; ++nt)
@@ -235,7 +244,9 @@ __global__ void __launch_bounds__(kWarps * 32, 2) attention_rows_kernel(const __
     for (int x = 1; x <= 2; x *= 2)
 #pragma unroll
       for (int h = 0; h < 2; ++h) top[h] = fmaxf(top[h], __shfl_xor_sync(0xffffffffu, top[h], x));
-    if (__any_sync(0xffffffffu, top[0] > m[0] || top[1] > m[1])) {
+    // The reference follows the maximum when that has grown by more than 8 (log2
+    // units): probabilities of up to 2^8 cost the fp32 sums nothing.
+    if (__any_sync(0xffffffffu, top[0] > m[0] + 8.f || top[1] > m[1] + 8.f)) {
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
         const float to = fmaxf(m[h], top[h]);
@@ -274,16 +285,16 @@ __global__ void __launch_bounds__(kWarps * 32, 2) attention_rows_kernel(const __
       const uint32_t* w1 = &vv[1].x;
       const uint32_t* w2 = &vv[2].x;
       const uint32_t* w3 = &vv[3].x;
+      uint32_t b0[8], b1[8];
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
+      for (int i = 0; i < 8; ++i) {
+        const uint32_t sel = i & 1 ? 0x7632u : 0x5410u;
+        b0[i] = __byte_perm(w0[i / 2], w1[i / 2], sel), b1[i] = __byte_perm(w2[i / 2], w3[i / 2], sel);
+      }
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          const uint32_t sel = e ? 0x7632u : 0x5410u;
-          const uint32_t b0 = __byte_perm(w0[i], w1[i], sel), b1 = __byte_perm(w2[i], w3[i], sel);
-          float(&d)[4] = o[8 * c + 2 * i + e];
-          mma_16816(d, hi[0], hi[1], hi[2], hi[3], b0, b1);
-          mma_16816(d, lo[0], lo[1], lo[2], lo[3], b0, b1);
-        }
+      for (int i = 0; i < 8; ++i) mma_16816(o[8 * c + i], hi[0], hi[1], hi[2], hi[3], b0[i], b1[i]);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) mma_16816(o[8 * c + i], lo[0], lo[1], lo[2], lo[3], b0[i], b1[i]);
     }
   }
   // ---- join, over the rings once every warp is through with its own
