@@ -1177,7 +1177,10 @@ tern_status tern_attention(const tern_attention_args* args, tern_stream_t stream
     ta.by_pairs = div_by(unsigned(pairs));
     ta.by_heads = div_by(unsigned(t.H));
     ta.by_group = div_by(unsigned(t.H / t.Hkv));
-    ta.wait_limit_ns = g_wait_limit_ns.load();
+    // Some warps wait for others through whole units: the time of a launch
+    // (1.5 us a key tile; 8 allowed) comes on top of the limit.
+    const double launch_ns = std::min(8000. * double(rounds) * double(tiles), 1e18);
+    ta.wait_limit_ns = std::min<unsigned long long>(g_wait_limit_ns.load(), 1ull << 60) + (unsigned long long)(launch_ns);
     ta.status = ds->status;
     e = launch_attention_tile(ta, reinterpret_cast<cudaStream_t>(stream));
   }

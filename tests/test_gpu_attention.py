@@ -206,3 +206,18 @@ def test_two_streams_at_once():
     torch.cuda.synchronize()
     assert all(torch.equal(o, wa) for o in oa) and all(torch.equal(o, wb) for o in ob)
     assert tern.device_status() == 0
+
+
+def test_units_longer_than_the_wait_limit():
+    """The limit bounds waits that make no progress: a unit of many keys may
+    take longer than it (200 key tiles, some 300 us; heads of two query tiles and of one)."""
+    q, k, v = inputs(1, 300, 25600, 80, 5, 64)
+    want = tern.attention(q, k, v)
+    torch.cuda.synchronize()
+    tern.set_wait_limit_ns(50_000)
+    try:
+        got = tern.attention(q, k, v)
+        assert tern.device_status() == 0
+    finally:
+        tern.set_wait_limit_ns(1_000_000_000)
+    assert torch.equal(got, want)
