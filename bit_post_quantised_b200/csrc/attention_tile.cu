@@ -379,6 +379,8 @@ __global__ void __launch_bounds__(kThreads, 1) attention_tile_kernel(const __gri
         }
         acc[0] = add2(acc[0], acc[1]);
         sum += acc[0].x + acc[0].y;
+        // The maximum itself overflowed in log2 units: against -inf every probability was 0.
+        if (base == -INFINITY) sum = NAN;
       }
       if (!ok) break;
       if (x.n == 0) continue;

@@ -221,3 +221,21 @@ def test_units_longer_than_the_wait_limit():
     finally:
         tern.set_wait_limit_ns(1_000_000_000)
     assert torch.equal(got, want)
+
+
+@pytest.mark.parametrize("Lq", [2, 300, 1700])
+def test_scaled_scores_that_overflow_give_nan_rows(Lq):
+    """Finite scores whose product with the scale is not: their rows are NaN, the others as before."""
+    q, k, v = inputs(1, Lq, 200, 2, 2, 64)
+    q[0, 1], k[0, 5] = 0.0, 0.0
+    want = tern.attention(q, k, v, scale=2.0 ** 40)
+    q[0, 1, :, 3] = 2.0 ** 60
+    k[0, 5, :, 3] = 2.0 ** 60
+    k[0, :5, :, 3] = 0.0
+    k[0, 6:, :, 3] = 0.0
+    q[0, 0, :, 3] = 0.0
+    q[0, 2:, :, 3] = 0.0
+    got = tern.attention(q, k, v, scale=2.0 ** 40)
+    assert torch.isnan(got[0, 1]).all()
+    rest = torch.arange(Lq, device="cuda") != 1
+    assert torch.isfinite(got[0, rest]).all() and torch.isfinite(want).all()
