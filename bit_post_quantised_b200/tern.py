@@ -512,20 +512,24 @@ def rope(xs: Sequence[torch.Tensor], cs: torch.Tensor, halves: bool = False,
     if cs.dtype is not torch.float32 or len(table) != 3 or table[2] != 2 or not cs.is_contiguous():
         raise ValueError("cs must be contiguous fp32 [rows, P, 2]")
     raw = _launch_on((*xs, cs, *(outs or ())), stream)
+    B, L = (shape[0], shape[1]) if nd == 4 else (1, shape[0])
+    D = shape[-1]
+    args = []
     if outs is None:
         outs = [_empty_as(x, stream) for x in xs]
-    elif len(outs) != len(xs):
-        raise ValueError("one output per tensor")
-    args = []
-    for x, y, (at, heads, sx) in zip(xs, outs, parts):
-        sy = y.stride()
-        if y.shape != x.shape or y.dtype is not torch.bfloat16 or (sy[-1] != 1 and shape[-1] > 1):
-            raise ValueError("an output is bf16 of its input's shape with adjacent channels")
-        if nd == 3:
-            sy = (0, *sy)
-        args += (at, y.data_ptr(), heads, sx[0], sx[1], sx[2], sy[0], sy[1], sy[2])
-    B, L = (shape[0], shape[1]) if nd == 4 else (1, shape[0])
-    _check(lib().tern_rope(struct.pack("2P7q" * len(xs), *args), len(xs), B, L, shape[-1], cs.data_ptr(), table[0],
+        for y, (at, heads, sx) in zip(outs, parts):
+            args += (at, y.data_ptr(), heads, sx[0], sx[1], sx[2], L * heads * D, heads * D, D)
+    else:
+        if len(outs) != len(xs):
+            raise ValueError("one output per tensor")
+        for x, y, (at, heads, sx) in zip(xs, outs, parts):
+            sy = y.stride()
+            if y.shape != x.shape or y.dtype is not torch.bfloat16 or (sy[-1] != 1 and D > 1):
+                raise ValueError("an output is bf16 of its input's shape with adjacent channels")
+            if nd == 3:
+                sy = (0, *sy)
+            args += (at, y.data_ptr(), heads, sx[0], sx[1], sx[2], sy[0], sy[1], sy[2])
+    _check(lib().tern_rope(struct.pack("2P7q" * len(xs), *args), len(xs), B, L, D, cs.data_ptr(), table[0],
                            table[1], 1 if halves else 0, raw))
     return list(outs)
 
@@ -600,42 +604,50 @@ def gated_residual_norm(x: torch.Tensor, o: torch.Tensor, *, gate: Optional[torc
     G = -(-M // T) if T > 0 else 0
     mod_ld = K
     apart = None
-    for name, t in (("gate", gate), ("scale", scale), ("shift", shift)):
+    at = [0, 0, 0]  # addresses of the modulation rows
+    for i, t in enumerate((gate, scale, shift)):
         if t is not None:
-            s = _bf16(name, t, (1, 2))
+            s = _bf16("gate, scale or shift", t, (1, 2))
             sh = t.shape
             if sh[-1] != K or (sh[0] if len(sh) == 2 else 1) < G:
-                raise ValueError(f"{name} holds fewer than the {G} modulation rows of {K} values that {M} rows at {T} tokens "
-                                 "per row need")
+                raise ValueError(f"{('gate', 'scale', 'shift')[i]} holds fewer than the {G} modulation rows of {K} values that "
+                                 f"{M} rows at {T} tokens per row need")
             if G > 1:
                 if apart is not None and s[0] != apart:
                     raise ValueError("gate, scale and shift rows must be the same distance apart")
                 apart = mod_ld = s[0]
-    for name, t in (("post_weight", post_weight), ("pre_weight", pre_weight)):
-        if t is not None:
-            _bf16(name, t, (1,))
-            if t.shape[0] != K:
-                raise ValueError(f"{name} must hold {K} values")
+            at[i] = t.data_ptr()
+    post_at = pre_at = 0
+    if post_weight is not None:
+        _bf16("post_weight", post_weight, (1,))
+        post_at = post_weight.data_ptr()
+    if pre_weight is not None:
+        _bf16("pre_weight", pre_weight, (1,))
+        pre_at = pre_weight.data_ptr()
+    for w in (post_weight, pre_weight):
+        if w is not None and w.shape[0] != K:
+            raise ValueError(f"post_weight and pre_weight must hold {K} values")
     raw = _launch_on((x, o, gate, scale, shift, post_weight, pre_weight, x_out, h), stream)
-    sxo = sh = (K, 1)
+    ld_xo = ld_h = K
     if x_out is None:
         x_out = _empty_as(x, stream)
     else:
-        sxo = _bf16("x_out", x_out, (2,))
+        ld_xo = _bf16("x_out", x_out, (2,))[0]
         if x_out.shape != shape:
             raise ValueError("x_out has x's shape")
     if h is not None:
-        sh = _bf16("h", h, (2,))
+        ld_h = _bf16("h", h, (2,))[0]
         if h.shape != shape:
             raise ValueError("h has x's shape")
     elif pre_norm != NORM_NONE or scale is not None or shift is not None:
         h = _empty_as(x, stream)
-    lds = (sx[0], so[0], sxo[0], sh[0]) if M > 1 else (K, K, K, K)
-    p = lambda t: 0 if t is None else t.data_ptr()  # noqa: E731
+    ld_x, ld_o = sx[0], so[0]
+    if M <= 1:
+        ld_x = ld_o = ld_xo = ld_h = K
     _check(lib().tern_gated_residual_norm(
-        _RESIDUAL_NORM.pack(x.data_ptr(), o.data_ptr(), x_out.data_ptr(), p(h), M, K, *lds, residual_scale, post_norm,
-                            p(post_weight), post_eps, p(gate), 1 if gate_tanh else 0, pre_norm, p(pre_weight), pre_eps,
-                            p(scale), p(shift), mod_ld, T), raw))
+        _RESIDUAL_NORM.pack(x.data_ptr(), o.data_ptr(), x_out.data_ptr(), 0 if h is None else h.data_ptr(), M, K, ld_x, ld_o,
+                            ld_xo, ld_h, residual_scale, post_norm, post_at, post_eps, at[0], 1 if gate_tanh else 0, pre_norm,
+                            pre_at, pre_eps, at[1], at[2], mod_ld, T), raw))
     return x_out, h
 
 
