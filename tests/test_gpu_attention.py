@@ -239,3 +239,20 @@ def test_scaled_scores_that_overflow_give_nan_rows(Lq):
     assert torch.isnan(got[0, 1]).all()
     rest = torch.arange(Lq, device="cuda") != 1
     assert torch.isfinite(got[0, rest]).all() and torch.isfinite(want).all()
+
+
+@pytest.mark.parametrize("Lq,Lk,D", [(300, 200, 128), (300, 129, 64), (129, 400, 96), (513, 64, 128)])
+def test_many_units_with_empty_entries(Lq, Lk, D):
+    """Several units a CTA: of one query tile and of two, of no, one and more key tiles in turn."""
+    B, H = 13, 12
+    q, k, v = inputs(B, Lq, Lk, H, H, D, seed=3)
+    n = torch.tensor([0, Lk, 1, 0, 0, 127, 128, 129, 0, Lk, 5, Lk - 1, 0], dtype=torch.int32)
+    valid = torch.arange(Lk)[None] < n[:, None]
+    k[(~valid).cuda()] = float("nan")
+    v[(~valid).cuda()] = float("inf")
+    out = torch.full((B, Lq + 3, H, D), 9.0, dtype=torch.bfloat16, device="cuda")
+    o = tern.attention(q, k, v, kv_len=n.cuda(), out=out[:, :Lq])
+    k[(~valid).cuda()] = 0.0
+    v[(~valid).cuda()] = 0.0
+    close(o, q, k, v, kv_len=n)
+    assert (o[n == 0] == 0).all() and (out[:, Lq:] == 9).all()

@@ -147,3 +147,23 @@ def test_no_rows_another_stream_and_a_graph():
     torch.cuda.synchronize()
     want = tern.gated_residual_norm(x, o, pre_norm=1)
     assert torch.equal(a, want[0]) and torch.equal(b, want[1])
+
+
+@pytest.mark.parametrize("M,K,T", [(9001, 1032, 3000), (5003, 2312, 5003), (120007, 64, 999), (40010, 520, 40010)])
+def test_long_walks_give_each_row_what_a_short_call_gives(M, K, T):
+    """Many rows per CTA, strided and in place, against calls on a few hundred rows each."""
+    wide = rand((M, 2 * K), 1).cuda()
+    x, o = wide[:, :K], rand((M, K), 2).cuda()
+    G = -(-M // T)
+    gate, scale, shift = (rand((G, K), 3 + i, 0.5).cuda() for i in range(3))
+    kw = dict(post_norm=tern.NORM_RMS, pre_norm=tern.NORM_LAYER)
+    keep = wide[:, K:].clone()
+    want = [torch.empty(M, K, dtype=torch.bfloat16, device="cuda") for _ in range(2)]
+    for m in range(0, M, 333):
+        for g in range(m // T, -(-min(m + 333, M) // T)):
+            a, b = max(m, g * T), min(m + 333, M, (g + 1) * T)
+            tern.gated_residual_norm(x[a:b], o[a:b], gate=gate[g], scale=scale[g], shift=shift[g], x_out=want[0][a:b],
+                                     h=want[1][a:b], **kw)
+    got = tern.gated_residual_norm(x, o, gate=gate, scale=scale, shift=shift, tokens_per_row=T, x_out=x, h=o, **kw)
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+    assert torch.equal(wide[:, K:], keep)
