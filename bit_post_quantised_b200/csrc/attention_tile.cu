@@ -22,6 +22,12 @@
 //                   in the next unit already (written by those themselves:
 //                   4096 x 512 +5%, 4096 x 77 +10%)
 //
+// Where units leave SMs idle (few query rows, many keys), a cluster of 2 to 8
+// CTAs shares the keys of one: each runs its own key tiles, leaves O and (m,
+// sum) in its ring once that is done with, and joins a part of the rows through
+// distributed shared memory (2 x 300 x 4000 x 6 heads of 64: 50 -> 21 us, 512 x
+// 16,384 x 8 of 128: 205 -> 64).  No workspace, and the same order every time.
+//
 // The reference m only follows the running maximum when that has grown by
 // more than 8 in log2 units: until then probabilities are at most 2^8, which
 // costs nothing in fp32 sums or in bf16's relative precision, and O needs no
@@ -164,6 +170,18 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
   return d;
 }
 
+__device__ __forceinline__ float2 ld_cluster_f2(uint32_t addr) {
+  float2 v;
+  asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];" : "=f"(v.x), "=f"(v.y) : "r"(addr) : "memory");
+  return v;
+}
+
+__device__ __forceinline__ float4 ld_cluster_f4(uint32_t addr) {
+  float4 v;
+  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(addr) : "memory");
+  return v;
+}
+
 // Waits like mbar_wait, in little code: the issuers' and the softmax warps'
 // loops are long enough to be bound by instruction fetches where every wait
 // carries its polling loop.
@@ -188,9 +206,10 @@ struct Unit {
   int b, h, hk, q0;
   int nq;   // query tiles with a row
   int len;  // keys before kv_len
+  int j0;   // first key tile
   int n;    // key tiles
 };
-template <bool MASK>
+template <bool MASK, bool SPLIT>
 __device__ __forceinline__ Unit unit_of(const AttnTileArgs& t, int u) {
   const AttnArgs& a = t.a;
   Unit x;
@@ -201,11 +220,73 @@ __device__ __forceinline__ Unit unit_of(const AttnTileArgs& t, int u) {
   x.q0 = (u - bh * t.pairs) * 2 * kBM;
   x.nq = x.q0 + kBM < a.Lq ? 2 : 1;
   x.len = MASK && a.kv_len ? max(0, min(a.Lk, a.kv_len[x.b])) : a.Lk;
+  x.j0 = 0;
   x.n = (x.len + kBN - 1) / kBN;
+  if constexpr (SPLIT) {  // this CTA's share
+    const int share = (x.n + t.splits - 1) / t.splits;
+    x.j0 = min(x.n, int(cluster_ctarank()) * share);
+    x.n = min(share, x.n - x.j0);
+  }
   return x;
 }
 
-template <int DP, bool MASK>
+// Joins the shares that a cluster's NS CTAs left in their shared memory (each
+// row's O, kRow floats apart, and its (m, sum)): this CTA's part of the rows,
+// by the threads of the softmax warps.  A thread takes eight channels of a
+// row at a time; all that it needs from the other CTAs for up to 8 / NS of
+// them is asked for before the first is used, since that is latency.
+template <int DP, int NS>
+__device__ __forceinline__ void join(uint32_t ring, int stats, int row_floats, int rows, float sl, uint16_t* o, const AttnArgs& a) {
+  constexpr int kGroups = DP / 8, kItems = 8 / NS, kMine = 2 * kBM / NS;  // rows of this CTA
+  constexpr int kTurns = kMine * kGroups / (256 * kItems);
+  static_assert(kTurns * 256 * kItems == kMine * kGroups, "whole turns");
+  const int first = int(cluster_ctarank()) * kMine;
+#pragma unroll 1
+  for (int turn = 0; turn < kTurns; ++turn) {
+    float2 ms[kItems][NS];
+    float4 v[kItems][NS][2];
+#pragma unroll
+    for (int n = 0; n < kItems; ++n) {
+      const int k = (turn * kItems + n) * 256 + int(threadIdx.x), row = first + k / kGroups, ch = k % kGroups * 8;
+#pragma unroll
+      for (int p = 0; p < NS; ++p) {
+        ms[n][p] = ld_cluster_f2(mapa_shared(ring + uint32_t(stats + 8 * row), p));
+        const uint32_t at = mapa_shared(ring + uint32_t((row * row_floats + ch) * 4), p);
+        v[n][p][0] = ld_cluster_f4(at);
+        v[n][p][1] = ld_cluster_f4(at + 16);
+      }
+    }
+#pragma unroll
+    for (int n = 0; n < kItems; ++n) {
+      const int k = (turn * kItems + n) * 256 + int(threadIdx.x), row = first + k / kGroups, ch = k % kGroups * 8;
+      float top = -INFINITY, total = 0.f, acc[8];
+#pragma unroll
+      for (int p = 0; p < NS; ++p) top = fmaxf(top, ms[n][p].x);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) acc[e] = 0.f;
+#pragma unroll
+      for (int p = 0; p < NS; ++p) {
+        // Without a valid key there O was not written; a NaN score's sum is NaN, and the row with it.
+        const bool none = ms[n][p].x == -INFINITY;
+        const float f = none ? 1.f : exp2_fast((ms[n][p].x - top) * sl);
+        total = fmaf(ms[n][p].y, f, total);
+        const float w[8] = {v[n][p][0].x, v[n][p][0].y, v[n][p][0].z, v[n][p][0].w,
+                            v[n][p][1].x, v[n][p][1].y, v[n][p][1].z, v[n][p][1].w};
+#pragma unroll
+        for (int e = 0; e < 8; ++e) acc[e] = none ? acc[e] : fmaf(w[e], f, acc[e]);
+      }
+      const float inv = total == 0.f ? 0.f : 1.f / total;
+      if (row < rows && ch < a.D)
+        *reinterpret_cast<uint4*>(o + (long long)row * a.o_l + ch) =
+            make_uint4(pack2(acc[0] * inv, acc[1] * inv), pack2(acc[2] * inv, acc[3] * inv), pack2(acc[4] * inv, acc[5] * inv),
+                       pack2(acc[6] * inv, acc[7] * inv));
+    }
+  }
+}
+
+// SPLIT: the CTAs of a cluster share the keys of one unit, each its own run of
+// key tiles, and join their (m, sum, O) through distributed shared memory.
+template <int DP, bool MASK, bool SPLIT>
 __global__ void __launch_bounds__(kThreads, 1) attention_tile_kernel(const __grid_constant__ AttnTileArgs t) {
   using C = TileShape<DP>;
   constexpr int S = C::kStages;
@@ -234,7 +315,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_tile_kernel(const __gri
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t smem_base = (smem_u32(dyn_smem) + 1023u) & ~1023u;
   const uint32_t ring = smem_base + 2 * C::kTile;
-  const int units = t.units, u0 = int(blockIdx.x), ustep = int(gridDim.x);
+  const int units = t.units, u0 = SPLIT ? int(blockIdx.x) / t.splits : int(blockIdx.x), ustep = SPLIT ? units : int(gridDim.x);
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < 2; ++i) {
@@ -282,9 +363,10 @@ __global__ void __launch_bounds__(kThreads, 1) attention_tile_kernel(const __gri
     const float2 sl2 = make_float2(sl, sl);
     uint32_t sp = 0, fp = 1;  // phases of s_full and o_free
     int mt = 0;  // key tiles so far (the slot and phase of the validity words)
+    float m = -INFINITY, sum = 0.f;
     bool ok = true;
     for (int u = u0; u < units && ok; u += ustep) {
-      const Unit x = unit_of<MASK>(t, u);
+      const Unit x = unit_of<MASK, SPLIT>(t, u);
       if (i >= x.nq) {
         if constexpr (MASK) {  // not this warp's keys, but its turn in the slots
           for (int j = 0; j < x.n && ok; ++j, ++mt) {
@@ -295,7 +377,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_tile_kernel(const __gri
         }
         continue;
       }
-      float m = -INFINITY, sum = 0.f;
+      m = -INFINITY, sum = 0.f;
       for (int j = 0; j < x.n; ++j) {
         ok = __all_sync(0xffffffffu, bar_wait(smem_u32(&s_full[i]), sp, lim, st));
         if (!ok) break;
@@ -305,7 +387,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_tile_kernel(const __gri
 #pragma unroll
         for (int c = 0; c < 4; ++c) tmem_ld32(ts + 32 * c, v[c]);
         tmem_wait_ld();
-        if (MASK || x.len - j * kBN < kBN) {
+        if (MASK || x.len - (x.j0 + j) * kBN < kBN) {
           uint32_t w[4];  // validity of the tile's keys
           if constexpr (MASK) {
             const int ms = mt % kMaskSlots;
@@ -317,7 +399,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_tile_kernel(const __gri
             if (lane == 0) mbar_arrive(smem_u32(&m_empty[ms]));
             ++mt;
           } else {
-            const int rem = x.len - j * kBN;
+            const int rem = x.len - (x.j0 + j) * kBN;
 #pragma unroll
             for (int c = 0; c < 4; ++c) w[c] = rem >= 32 * c + 32 ? ~0u : rem <= 32 * c ? 0u : (1u << (rem - 32 * c)) - 1u;
           }
@@ -383,7 +465,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_tile_kernel(const __gri
         if (base == -INFINITY) sum = NAN;
       }
       if (!ok) break;
-      if (x.n == 0) continue;
+      if (SPLIT || x.n == 0) continue;
       // The rows' sums to the output warps, once they are through with the unit before.
       ok = __all_sync(0xffffffffu, bar_wait(smem_u32(&o_free[i]), fp, lim, st));
       if (!ok) break;
@@ -392,6 +474,41 @@ __global__ void __launch_bounds__(kThreads, 1) attention_tile_kernel(const __gri
       __syncwarp();
       if (lane == 0) mbar_arrive(smem_u32(&sum_full[i]));
     }
+    if constexpr (SPLIT) {
+      const Unit x = unit_of<MASK, SPLIT>(t, u0);
+      // Every product of this CTA is done, so its ring is free: O and (m, sum)
+      // of its rows go there.
+      for (int k = 0; k < x.nq && x.n > 0 && ok; ++k)
+        ok = __all_sync(0xffffffffu, bar_wait(smem_u32(&o_done[k]), 0, lim, st));
+      constexpr int kRow = DP + 4;  // floats: a warp's rows start in different banks
+      constexpr int kStats = 2 * kBM * kRow * 4;
+      static_assert(kStats + 2 * kBM * 8 <= S * C::kTile, "the join fits the ring");
+      const int r = i * kBM + (warp & 3) * 32 + lane;
+      if (ok) {
+        tc_fence_after();
+        const uint32_t row = ring + uint32_t(r * kRow * 4);
+        if (i < x.nq && x.n > 0)
+#pragma unroll 1
+          for (int c = 0; c < DP; c += 32) {
+            uint32_t y[32];
+            tmem_ld32(to + c, y);
+            tmem_wait_ld();
+#pragma unroll
+            for (int e = 0; e < 32; e += 4)
+              asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(row + uint32_t(4 * (c + e))), "r"(y[e]),
+                           "r"(y[e + 1]), "r"(y[e + 2]), "r"(y[e + 3])
+                           : "memory");
+          }
+        asm volatile("st.shared.v2.f32 [%0], {%1, %2};" ::"r"(ring + uint32_t(kStats + 8 * r)), "f"(m), "f"(sum) : "memory");
+      }
+      cluster_sync();
+      const int rows = min(2 * kBM, a.Lq - x.q0);
+      uint16_t* const o = a.o + x.b * a.o_b + (long long)x.q0 * a.o_l + x.h * a.o_h;
+      if (t.splits == 2) join<DP, 2>(ring, kStats, kRow, rows, sl, o, a);
+      else if (t.splits == 4) join<DP, 4>(ring, kStats, kRow, rows, sl, o, a);
+      else join<DP, 8>(ring, kStats, kRow, rows, sl, o, a);
+      cluster_sync_relaxed();  // no CTA leaves while another may still read its shared memory
+    }
   } else if (warp >= 12) {
     // ------------------------------------------------------ output
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOutRegs));
@@ -399,8 +516,8 @@ __global__ void __launch_bounds__(kThreads, 1) attention_tile_kernel(const __gri
     const uint32_t lane_off = uint32_t((warp & 3) * 32) << 16;
     uint32_t ph = 0;  // bit i: phase of o_done and sum_full
     bool ok = true;
-    for (int u = u0; u < units && ok; u += ustep) {
-      const Unit x = unit_of<MASK>(t, u);
+    for (int u = u0; !SPLIT && u < units && ok; u += ustep) {
+      const Unit x = unit_of<MASK, SPLIT>(t, u);
 #pragma unroll 1
       for (int i = 0; i < x.nq; ++i) {
         const uint32_t to = tmem + lane_off + 256 + i * DP;
@@ -491,7 +608,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_tile_kernel(const __gri
       const uint32_t own_bar = lane == 2 ? smem_u32(&p_full[0][0]) : lane == 3 ? smem_u32(&q_full[0]) : smem_u32(&o_free[0]);
       auto next_unit = [&](int u, Unit& x) {  // the first unit from u on with keys
         for (; u < units; u += ustep) {
-          x = unit_of<MASK>(t, u);
+          x = unit_of<MASK, SPLIT>(t, u);
           if (x.n > 0) break;
         }
         return u;
@@ -582,15 +699,15 @@ __global__ void __launch_bounds__(kThreads, 1) attention_tile_kernel(const __gri
         int it = 0, qc[2] = {0, 0};
         bool ok = true;
         for (int u = u0; u < units && ok; u += ustep) {
-          const Unit x = unit_of<MASK>(t, u);
+          const Unit x = unit_of<MASK, SPLIT>(t, u);
           for (int k = 0; k < 2 * x.n && ok; ++k) {
             const int s = it % S;
             ok = mbar_wait(smem_u32(&kv_empty[s]), ((it / S) & 1) ^ 1, lim, st);
             if (!ok) break;
             if (k & 1)
-              load(ring + s * C::kTile, &t.tv, (k >> 1) * kBN, x.hk * t.v_h, x.b * t.v_b, &kv_full[s]);
+              load(ring + s * C::kTile, &t.tv, (x.j0 + (k >> 1)) * kBN, x.hk * t.v_h, x.b * t.v_b, &kv_full[s]);
             else
-              load(ring + s * C::kTile, &t.tk, (k >> 1) * kBN, x.hk * t.k_h, x.b * t.k_b, &kv_full[s]);
+              load(ring + s * C::kTile, &t.tk, (x.j0 + (k >> 1)) * kBN, x.hk * t.k_h, x.b * t.k_b, &kv_full[s]);
             ++it;
             if (k == 0) {
 #pragma unroll
@@ -615,14 +732,14 @@ __global__ void __launch_bounds__(kThreads, 1) attention_tile_kernel(const __gri
       int mt = 0;
       bool ok = true;
       for (int u = u0; u < units && ok; u += ustep) {
-        const Unit x = unit_of<MASK>(t, u);
+        const Unit x = unit_of<MASK, SPLIT>(t, u);
         const uint8_t* mask = a.key_mask ? a.key_mask + x.b * a.mask_ld : nullptr;
         for (int j = 0; j < x.n && ok; ++j, ++mt) {
           const int ms = mt % kMaskSlots, it = 2 * mt + 1, vs = it % S;
           uint32_t w[4];
 #pragma unroll
           for (int c = 0; c < 4; ++c) {
-            const int key = j * kBN + 32 * c + lane;
+            const int key = (x.j0 + j) * kBN + 32 * c + lane;
             w[c] = __ballot_sync(0xffffffffu, key < x.len && (!mask || mask[key]));
           }
           ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(&m_empty[ms]), ((mt / kMaskSlots) & 1) ^ 1, lim, st));
@@ -653,6 +770,13 @@ __global__ void __launch_bounds__(kThreads, 1) attention_tile_kernel(const __gri
       }
     }
   }
+  if constexpr (SPLIT) {
+    if (warp >= 8) {  // the softmax warps' two
+      __syncwarp();
+      cluster_sync();
+      cluster_sync_relaxed();
+    }
+  }
   // Every role is done with TMEM and the barriers.
   __syncthreads();
   if (warp == 8) {
@@ -661,7 +785,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_tile_kernel(const __gri
   }
 }
 
-template <int DP, bool MASK>
+template <int DP, bool MASK, bool SPLIT>
 cudaError_t launch_one(const AttnTileArgs& t, cudaStream_t stream) {
   using C = TileShape<DP>;
   // Per device: the kernel's shared memory, and that it was compiled to the
@@ -673,22 +797,28 @@ cudaError_t launch_one(const AttnTileArgs& t, cudaStream_t stream) {
   if (e != cudaSuccess) return e;
   if (ready_dev != dev) {
     cudaFuncAttributes f;
-    if ((e = cudaFuncGetAttributes(&f, attention_tile_kernel<DP, MASK>)) != cudaSuccess) return e;
+    if ((e = cudaFuncGetAttributes(&f, attention_tile_kernel<DP, MASK, SPLIT>)) != cudaSuccess) return e;
     if (f.numRegs * kThreads < 256 * kSoftmaxRegs + 128 * kOtherRegs + 128 * kOutRegs) return cudaErrorInvalidConfiguration;
-    e = cudaFuncSetAttribute(attention_tile_kernel<DP, MASK>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
+    e = cudaFuncSetAttribute(attention_tile_kernel<DP, MASK, SPLIT>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
     if (e != cudaSuccess) return e;
     ready_dev = dev;
   }
-  return launch_pdl(attention_tile_kernel<DP, MASK>, dim3(unsigned(t.units < t.ctas ? t.units : t.ctas)), dim3(kThreads),
-                    C::kSmem, stream, 1, t);
+  const int grid = SPLIT ? t.units * t.splits : t.units < t.ctas ? t.units : t.ctas;
+  return launch_pdl(attention_tile_kernel<DP, MASK, SPLIT>, dim3(unsigned(grid)), dim3(kThreads), C::kSmem, stream,
+                    SPLIT ? unsigned(t.splits) : 1u, t);
 }
 
 }  // namespace
 
-cudaError_t launch_attention_tile(const AttnTileArgs& t, cudaStream_t stream) {
+template <bool SPLIT>
+static cudaError_t launch_tile(const AttnTileArgs& t, cudaStream_t stream) {
   const bool mask = t.a.kv_len || t.a.key_mask;
-  if (t.a.D <= 64) return mask ? launch_one<64, true>(t, stream) : launch_one<64, false>(t, stream);
-  return mask ? launch_one<128, true>(t, stream) : launch_one<128, false>(t, stream);
+  if (t.a.D <= 64) return mask ? launch_one<64, true, SPLIT>(t, stream) : launch_one<64, false, SPLIT>(t, stream);
+  return mask ? launch_one<128, true, SPLIT>(t, stream) : launch_one<128, false, SPLIT>(t, stream);
+}
+
+cudaError_t launch_attention_tile(const AttnTileArgs& t, cudaStream_t stream) {
+  return t.splits > 1 ? launch_tile<true>(t, stream) : launch_tile<false>(t, stream);
 }
 
 }  // namespace tern

@@ -221,6 +221,7 @@ struct alignas(64) AttnTileArgs {
   int pairs;  // of 128-row query tiles, per head
   int units;  // pairs * B * H
   int ctas;   // resident at once
+  int splits;  // CTAs (a cluster) that share the keys of a unit: 1, or 2 to 8 where all units are resident at once
   int o_sectors;  // o's rows are made of whole 32-byte sectors
   DivBy by_pairs, by_heads, by_group;  // pairs, H, H / Hkv
   unsigned long long wait_limit_ns;

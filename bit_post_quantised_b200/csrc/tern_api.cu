@@ -1156,7 +1156,20 @@ tern_status tern_attention(const tern_attention_args* args, tern_stream_t stream
   const int64_t blocks = (t.Lk + 64 * splits - 1) / (64 * splits), tiles = (t.Lk + 127) / 128;
   const bool wide = t.D > 64;
   const double rows_us = 2.5 + (splits > 1 ? 1. : 0.) + double(waves) * (wide ? 2.5 + 1.05 * blocks : 1.2 + 0.65 * blocks);
-  const double tiles_us = (wide ? 3.3 : 4.9) + (wide ? 1.47 : 0.98) * double(rounds) * double(tiles);
+  // Where units leave SMs idle, a cluster of CTAs shares the keys of each, as
+  // far as all clusters are resident at once (of 8 CTAs with an SM each: 64
+  // CTAs in one wave, 128 in two).  The join takes 2.5 us and 1.6 a CTA.
+  // Measured (us, 1 | 2 | 4 | 8 CTAs): 256 x 4608 x 8 heads of 128 61 | 39 | 27 |
+  // 25, 512 x 16,384 x 8 206 | 113 | 64 | -, 1024 x 1024 x 8 18 | 16.6 | 17.5 |
+  // -, 256 x 512 x 8 11 | 13 | 14 | 17, 2 x 300 x 4000 x 6 of 64 50 | 30 | 21 | -.
+  const double tile_us = wide ? (t.Lq > 128 ? 1.6 : 1.47) : t.Lq > 128 ? 1.4 : 0.98;
+  auto tiles_time = [&](int n) {
+    return (wide ? 3.3 : 4.9) + (n > 1 ? 2.5 + 1.6 * n : 0.) + tile_us * double(rounds) * double((tiles + n - 1) / n);
+  };
+  int tile_splits = 1;
+  for (int n = 2; n <= 8 && tile_units * n <= (n > 4 ? 64 : 128); n *= 2)
+    if (tiles_time(n) < tiles_time(tile_splits)) tile_splits = n;
+  const double tiles_us = tiles_time(tile_splits);
   const bool rows = rows_us <= tiles_us;
   cudaError_t e;
   if (rows || flat || t.Lk == 0) {
@@ -1172,6 +1185,7 @@ tern_status tern_attention(const tern_attention_args* args, tern_stream_t stream
     ta.pairs = int(pairs);
     ta.units = int(tile_units);
     ta.ctas = ds->sms;
+    ta.splits = tile_splits;
     ta.o_sectors = aligned(t.o, 32) && t.D % 16 == 0 && (t.B <= 1 || t.o_b % 16 == 0) && (t.Lq <= 1 || t.o_l % 16 == 0) &&
                    (t.H <= 1 || t.o_h % 16 == 0);
     ta.by_pairs = div_by(unsigned(pairs));

@@ -256,3 +256,36 @@ def test_many_units_with_empty_entries(Lq, Lk, D):
     v[(~valid).cuda()] = 0.0
     close(o, q, k, v, kv_len=n)
     assert (o[n == 0] == 0).all() and (out[:, Lq:] == 9).all()
+
+
+@pytest.mark.parametrize("B,Lq,Lk,H,Hkv,D", [(1, 256, 2700, 8, 8, 128), (1, 513, 2049, 4, 2, 96), (2, 300, 4000, 6, 3, 64),
+                                             (1, 1000, 1500, 5, 5, 40), (1, 129, 3333, 40, 40, 128), (3, 257, 1025, 8, 8, 128)])
+@pytest.mark.parametrize("kind", ["none", "len", "mask"])
+def test_few_units_of_many_keys(B, Lq, Lk, H, Hkv, D, kind):
+    """A cluster shares the keys of a unit: shares without a key, ends inside a
+    tile, NaN and infinities in masked places, entries without a key, the
+    rows behind the last one as they were."""
+    if kind != "none":
+        B = 3
+    q, k, v = inputs(B, Lq, Lk, H, Hkv, D, seed=21)
+    n = m = None
+    valid = torch.ones(B, Lk, dtype=torch.bool)
+    if kind == "len":
+        n = torch.tensor([Lk // 2 + 3, 0, 130], dtype=torch.int32)
+        valid &= torch.arange(Lk)[None] < n[:, None]
+    elif kind == "mask":
+        m = torch.rand(B, Lk, generator=torch.Generator().manual_seed(Lq)) < 0.5
+        m[1, : Lk // 2] = False
+        m[2] = False
+        valid &= m
+    bad = (~valid).cuda()
+    kd, vd = k.clone(), v.clone()
+    kd[bad] = float("nan")
+    vd[bad] = float("inf")
+    n, m = (None if n is None else n.cuda()), (None if m is None else m.cuda())
+    out = torch.full((B, Lq + 2, H, D), 5.0, dtype=torch.bfloat16, device="cuda")
+    o = tern.attention(q, kd, vd, kv_len=n, key_mask=m, out=out[:, :Lq])
+    close(o, q, k, v, kv_len=n, key_mask=m)
+    assert (o[~valid.any(1)] == 0).all() and (out[:, Lq:] == 5).all()
+    for _ in range(3):
+        assert torch.equal(tern.attention(q, kd, vd, kv_len=n, key_mask=m), o)
