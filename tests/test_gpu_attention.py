@@ -289,3 +289,39 @@ def test_few_units_of_many_keys(B, Lq, Lk, H, Hkv, D, kind):
     assert (o[~valid.any(1)] == 0).all() and (out[:, Lq:] == 5).all()
     for _ in range(3):
         assert torch.equal(tern.attention(q, kd, vd, kv_len=n, key_mask=m), o)
+
+
+def test_shared_keys_on_two_streams_and_in_a_graph():
+    """Clusters that share a unit's keys: two such calls in flight together, a captured one replayed on new inputs."""
+    a, b = inputs(1, 256, 4608, 8, 8, 128), inputs(2, 300, 4000, 6, 3, 64)
+    wa, wb = tern.attention(*a), tern.attention(*b)
+    s, r = torch.cuda.Stream(), torch.cuda.Stream()
+    for st in (s, r):
+        st.wait_stream(torch.cuda.current_stream())
+    oa = [tern.attention(*a, stream=s) for _ in range(8)]
+    ob = [tern.attention(*b, stream=r) for _ in range(8)]
+    torch.cuda.synchronize()
+    assert all(torch.equal(o, wa) for o in oa) and all(torch.equal(o, wb) for o in ob)
+    out = torch.empty_like(wa)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        tern.attention(*a, out=out)
+    a[0].copy_(rand(a[0].shape, 5))
+    g.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(out, tern.attention(*a))
+    close(out, *a)
+
+
+def test_shared_keys_with_peaks_and_scores_that_are_not_finite():
+    q, k, v = inputs(1, 300, 4000, 4, 4, 128, std=3.0)
+    up = torch.linspace(-4, 4, 4000, device="cuda")[None, :, None, None]
+    for kk in ((k.float() + up * q.float().mean(1, keepdim=True)).bfloat16(),
+               (k.float() - up * q.float().mean(1, keepdim=True)).bfloat16()):
+        close(tern.attention(q, kk, v, scale=0.5), q, kk, v, scale=0.5)
+    want = tern.attention(q, k, v)
+    q[0, 1, 0, 3] = float("nan")
+    got = tern.attention(q, k, v)
+    assert torch.isnan(got[0, 1, 0]).all()
+    got[0, 1, 0] = want[0, 1, 0]
+    assert torch.equal(got, want)
