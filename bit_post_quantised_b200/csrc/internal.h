@@ -228,9 +228,9 @@ struct alignas(64) AttnTileArgs {
   unsigned int* status;
 };
 cudaError_t launch_attention_tile(const AttnTileArgs& t, cudaStream_t stream);
-// One read of k and v for up to 16 packed query rows; see attention_rows.cu.
 // CTAs that share the keys of one unit (16 query rows of a key-value head) in the row kernel.
 int attention_rows_splits(long long units, long long Lk, int sms);
+// One read of k and v for up to 16 packed query rows; see attention_rows.cu.
 cudaError_t launch_attention_rows(const AttnArgs& a, int sms, cudaStream_t stream);
 
 }  // namespace tern
