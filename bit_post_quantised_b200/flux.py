@@ -155,8 +155,8 @@ class TernaryFlux:
             if p is not None:
                 W, b = p["kv"]
                 packed, scales = tern.quantize_pack(W.to(self.device), workloads.EPS, stream=stream)
-                self.context[i] = {"kv": (packed, scales, b.to(self.device)), "norm": p["norm"].to(self.device),
-                                   "gate": p["gate"].to(self.device)}
+                self.context[i] = {"kv": (packed, scales, b.to(self.device)), "dim": W.shape[1],
+                                   "norm": p["norm"].to(self.device), "gate": p["gate"].to(self.device)}
 
     def _lin(self, q, x, y, **epi):
         packed, scales, b = q
@@ -179,7 +179,15 @@ class TernaryFlux:
 
     def context_kv(self, context: torch.Tensor) -> Dict:
         """Keys and values [Lc, 2C] of the encoder's states context [Lc, dim]
-        for every double block that attends to them, in batched launches."""
+        for every double block that attends to them, in batched launches.
+        The library sees an address and takes K from the states' width, so what
+        does not fit the codes is refused here."""
+        for i, c in self.context.items():
+            scales = c["kv"][1]
+            if (context.dtype is not torch.bfloat16 or context.dim() != 2 or context.shape[1] != c["dim"]
+                    or not context.is_contiguous() or context.device != scales.device):
+                raise ValueError(f"double block {i} takes contiguous bf16 states [Lc, {c['dim']}] on {scales.device}; got "
+                                 f"{context.dtype} {tuple(context.shape)} on {context.device}")
         outs = {i: torch.empty(context.shape[0], c["kv"][1].shape[0], dtype=torch.bfloat16, device=self.device)
                 for i, c in self.context.items()}
         probs = [self._lin(c["kv"], context, outs[i]) for i, c in self.context.items()]

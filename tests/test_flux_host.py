@@ -8,6 +8,7 @@ from __future__ import annotations
 import math
 
 import numpy as np
+import pytest
 import torch
 
 from oracle import flux as OF
@@ -123,3 +124,22 @@ def test_parameter_count_matches_the_pages():
     total = ternary + biases + norms + io
     assert abs(total / 1e9 - 11.9) < 0.05
     assert abs(ternary / total - 0.995) < 2e-3
+
+
+@pytest.mark.parametrize("states", [
+    torch.zeros(5, 256, dtype=torch.bfloat16),                       # wider than the codes: they would be read past their end
+    torch.zeros(5, 128, dtype=torch.bfloat16),
+    torch.zeros(5, 192),                                             # fp32
+    torch.zeros(1, 5, 192, dtype=torch.bfloat16),
+    torch.zeros(192, 5, dtype=torch.bfloat16).T,
+    torch.zeros(5, 192, dtype=torch.bfloat16, device="meta"),        # another device
+])
+def test_states_that_do_not_fit_their_weights_are_refused(states):
+    cfg = workloads.FLUX_SMALL
+    model = object.__new__(flux.TernaryFlux)  # no GPU here: the codes of one block's projection alone
+    model.cfg, model.device, model.stream = cfg, torch.device("cpu"), None
+    n = 2 * cfg.hidden
+    model.context = {0: {"kv": (torch.zeros(n * 192 // 4, dtype=torch.uint8), torch.ones(n),
+                                torch.zeros(n, dtype=torch.bfloat16)), "dim": 192}}
+    with pytest.raises(ValueError, match="double block 0 takes"):
+        model.context_kv(states)
