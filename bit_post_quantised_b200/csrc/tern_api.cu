@@ -990,6 +990,65 @@ tern_status make_heads_map(CUtensorMap* map, const Heads& t, int* h_mul, int* b_
 const uint16_t* u16(const void* p) { return static_cast<const uint16_t*>(p); }
 uint16_t* u16w(void* p) { return static_cast<uint16_t*>(p); }
 
+// The kernel that takes a call, and the CTAs (a cluster) that share the keys of one of its units.
+struct AttnChoice {
+  bool rows;
+  int ctas;
+  int64_t pairs, tile_units, rounds, tiles;
+};
+
+AttnChoice choose_attention(const tern_attention_args& t, int sms) {
+  // Each kernel's time as it was measured, in us.  Rows: a start, and for every
+  // wave of its CTAs (two an SM) the 16-key blocks that a warp takes one after
+  // the other; tiles: a start, and for every round of units over the SMs its
+  // key tiles, however few of a tile's rows there are.  Measured (us, rows |
+  // tiles): 24 heads of 128, 512 keys: 32 queries 8.4 | 9.1, 64 queries 11.4 |
+  // 9.1; 4096 keys: 32 queries 23 | 50, 96 queries 39 | 50; 64 x 1 query of 8 heads, 4096
+  // keys 154 | 193; 4 heads of 64, 256 x 256 5.3 | 6.9; 24 heads of 64, 256 x 77
+  // 9.8 | 5.7.  (A tensor map has no dimension of stride 0: tokens that are one
+  // broadcast row take rows.)
+  const bool flat = (t.Lq > 1 && t.q_l == 0) || (t.Lk > 1 && (t.k_l == 0 || t.v_l == 0));
+  const int64_t pairs = (t.Lq + 255) / 256, tile_units = pairs * t.B * t.H;
+  const int64_t row_units = (t.Lq * (t.H / t.Hkv) + 15) / 16 * t.Hkv * t.B;
+  const int64_t rounds = (tile_units + sms - 1) / sms;
+  const int splits = attention_rows_splits(row_units, t.Lk, sms);
+  const int64_t waves = (row_units * splits + 2 * sms - 1) / (2 * sms);
+  const int64_t blocks = (t.Lk + 64 * splits - 1) / (64 * splits), tiles = (t.Lk + 127) / 128;
+  const bool wide = t.D > 64;
+  const double rows_us = 2.5 + (splits > 1 ? 1. : 0.) + double(waves) * (wide ? 2.5 + 1.05 * blocks : 1.2 + 0.65 * blocks);
+  // Where units leave SMs idle, a cluster of CTAs shares the keys of each, as
+  // far as all clusters are resident at once (of 8 CTAs with an SM each: 64
+  // CTAs in one wave, 128 in two).  The join takes 2.5 us and 1.6 a CTA.
+  // Measured (us, 1 | 2 | 4 | 8 CTAs): 256 x 4608 x 8 heads of 128 61 | 39 | 27 |
+  // 25, 512 x 16,384 x 8 206 | 113 | 64 | -, 1024 x 1024 x 8 18 | 16.6 | 17.5 |
+  // -, 256 x 512 x 8 11 | 13 | 14 | 17, 2 x 300 x 4000 x 6 of 64 50 | 30 | 21 | -.
+  const double tile_us = wide ? (t.Lq > 128 ? 1.6 : 1.47) : t.Lq > 128 ? 1.4 : 0.98;
+  auto tiles_time = [&](int n) {
+    return (wide ? 3.3 : 4.9) + (n > 1 ? 2.5 + 1.6 * n : 0.) + tile_us * double(rounds) * double((tiles + n - 1) / n);
+  };
+  int tile_splits = 1;
+  for (int n = 2; n <= 8 && tile_units * n <= (n > 4 ? 64 : 128); n *= 2)
+    if (tiles_time(n) < tiles_time(tile_splits)) tile_splits = n;
+  const bool rows = rows_us <= tiles_time(tile_splits) || flat || t.Lk == 0;
+  return {rows, rows ? splits : tile_splits, pairs, tile_units, rounds, tiles};
+}
+
+tern_status check_attention_sizes(const tern_attention_args& t) {
+  if (t.B < 0 || t.Lq < 0 || t.Lk < 0 || t.H < 0 || t.Hkv < 0 || t.D < 0)
+    return fail(TERN_ERR_INVALID_ARG, "negative size B=%lld Lq=%lld Lk=%lld H=%lld Hkv=%lld D=%lld", (long long)t.B,
+                (long long)t.Lq, (long long)t.Lk, (long long)t.H, (long long)t.Hkv, (long long)t.D);
+  if (t.D < 8 || t.D % 8 != 0 || t.D > kAttnMaxD)
+    return fail(TERN_ERR_UNSUPPORTED_SHAPE, "attention: need D %% 8 == 0 and 8 <= D <= %d, got %lld", kAttnMaxD, (long long)t.D);
+  if (t.B == 0 || t.Lq == 0 || t.H == 0) return TERN_OK;
+  const int64_t kMaxL = int64_t(1) << 30, kMaxBH = int64_t(1) << 20;
+  if (t.Hkv == 0 || t.H % t.Hkv != 0)
+    return fail(TERN_ERR_UNSUPPORTED_SHAPE, "attention: H must be a multiple of Hkv (H=%lld Hkv=%lld)", (long long)t.H,
+                (long long)t.Hkv);
+  if (t.Lq >= kMaxL || t.Lk >= kMaxL || t.B >= kMaxBH || t.H >= kMaxBH || t.B * t.H >= kMaxBH)
+    return fail(TERN_ERR_UNSUPPORTED_SHAPE, "attention: Lq and Lk are below 2^30, B * H below 2^20");
+  return TERN_OK;
+}
+
 }  // namespace
 
 tern_status tern_rope_table(const float* ids, int64_t L, int n_axes, const int* axis_dims, double theta, float* cs,
@@ -1092,18 +1151,8 @@ tern_status tern_rope(const tern_rope_tensor* tensors, int count, int64_t B, int
 tern_status tern_attention(const tern_attention_args* args, tern_stream_t stream) {
   if (!args) return fail(TERN_ERR_INVALID_ARG, "null args");
   const tern_attention_args& t = *args;
-  if (t.B < 0 || t.Lq < 0 || t.Lk < 0 || t.H < 0 || t.Hkv < 0 || t.D < 0)
-    return fail(TERN_ERR_INVALID_ARG, "negative size B=%lld Lq=%lld Lk=%lld H=%lld Hkv=%lld D=%lld", (long long)t.B,
-                (long long)t.Lq, (long long)t.Lk, (long long)t.H, (long long)t.Hkv, (long long)t.D);
-  if (t.D < 8 || t.D % 8 != 0 || t.D > kAttnMaxD)
-    return fail(TERN_ERR_UNSUPPORTED_SHAPE, "attention: need D %% 8 == 0 and 8 <= D <= %d, got %lld", kAttnMaxD, (long long)t.D);
+  if (tern_status e = check_attention_sizes(t); e != TERN_OK) return e;
   if (t.B == 0 || t.Lq == 0 || t.H == 0) return TERN_OK;
-  const int64_t kMaxL = int64_t(1) << 30, kMaxBH = int64_t(1) << 20;
-  if (t.Hkv == 0 || t.H % t.Hkv != 0)
-    return fail(TERN_ERR_UNSUPPORTED_SHAPE, "attention: H must be a multiple of Hkv (H=%lld Hkv=%lld)", (long long)t.H,
-                (long long)t.Hkv);
-  if (t.Lq >= kMaxL || t.Lk >= kMaxL || t.B >= kMaxBH || t.H >= kMaxBH || t.B * t.H >= kMaxBH)
-    return fail(TERN_ERR_UNSUPPORTED_SHAPE, "attention: Lq and Lk are below 2^30, B * H below 2^20");
   const float scale_log2 = t.scale * 1.44269504088896340736f;
   if (!(t.scale > 0.f) || !std::isfinite(scale_log2))
     return fail(TERN_ERR_INVALID_ARG, "scale must be > 0 and below 2^127 (scale=%g)", double(t.scale));
@@ -1138,41 +1187,9 @@ tern_status tern_attention(const tern_attention_args* args, tern_stream_t stream
   DeviceState* ds;
   tern_status s;
   if ((s = current_device(&dev, &ds)) != TERN_OK) return s;
-  // Each kernel's time as it was measured, in us.  Rows: a start, and for every
-  // wave of its CTAs (two an SM) the 16-key blocks that a warp takes one after
-  // the other; tiles: a start, and for every round of units over the SMs its
-  // key tiles, however few of a tile's rows there are.  Measured (us, rows |
-  // tiles): 24 heads of 128, 512 keys: 32 queries 8.4 | 9.1, 64 queries 11.4 |
-  // 9.1; 4096 keys: 32 queries 23 | 50, 96 queries 39 | 50; 64 x 1 query of 8 heads, 4096
-  // keys 154 | 193; 4 heads of 64, 256 x 256 5.3 | 6.9; 24 heads of 64, 256 x 77
-  // 9.8 | 5.7.  (A tensor map has no dimension of stride 0: tokens that are one
-  // broadcast row take rows.)
-  const bool flat = (t.Lq > 1 && t.q_l == 0) || (t.Lk > 1 && (t.k_l == 0 || t.v_l == 0));
-  const int64_t pairs = (t.Lq + 255) / 256, tile_units = pairs * t.B * t.H;
-  const int64_t row_units = (t.Lq * (t.H / t.Hkv) + 15) / 16 * t.Hkv * t.B;
-  const int64_t rounds = (tile_units + ds->sms - 1) / ds->sms;
-  const int splits = attention_rows_splits(row_units, t.Lk, ds->sms);
-  const int64_t waves = (row_units * splits + 2 * ds->sms - 1) / (2 * ds->sms);
-  const int64_t blocks = (t.Lk + 64 * splits - 1) / (64 * splits), tiles = (t.Lk + 127) / 128;
-  const bool wide = t.D > 64;
-  const double rows_us = 2.5 + (splits > 1 ? 1. : 0.) + double(waves) * (wide ? 2.5 + 1.05 * blocks : 1.2 + 0.65 * blocks);
-  // Where units leave SMs idle, a cluster of CTAs shares the keys of each, as
-  // far as all clusters are resident at once (of 8 CTAs with an SM each: 64
-  // CTAs in one wave, 128 in two).  The join takes 2.5 us and 1.6 a CTA.
-  // Measured (us, 1 | 2 | 4 | 8 CTAs): 256 x 4608 x 8 heads of 128 61 | 39 | 27 |
-  // 25, 512 x 16,384 x 8 206 | 113 | 64 | -, 1024 x 1024 x 8 18 | 16.6 | 17.5 |
-  // -, 256 x 512 x 8 11 | 13 | 14 | 17, 2 x 300 x 4000 x 6 of 64 50 | 30 | 21 | -.
-  const double tile_us = wide ? (t.Lq > 128 ? 1.6 : 1.47) : t.Lq > 128 ? 1.4 : 0.98;
-  auto tiles_time = [&](int n) {
-    return (wide ? 3.3 : 4.9) + (n > 1 ? 2.5 + 1.6 * n : 0.) + tile_us * double(rounds) * double((tiles + n - 1) / n);
-  };
-  int tile_splits = 1;
-  for (int n = 2; n <= 8 && tile_units * n <= (n > 4 ? 64 : 128); n *= 2)
-    if (tiles_time(n) < tiles_time(tile_splits)) tile_splits = n;
-  const double tiles_us = tiles_time(tile_splits);
-  const bool rows = rows_us <= tiles_us;
+  const AttnChoice c = choose_attention(t, ds->sms);
   cudaError_t e;
-  if (rows || flat || t.Lk == 0) {
+  if (c.rows) {
     e = launch_attention_rows(a, ds->sms, reinterpret_cast<cudaStream_t>(stream));
   } else {
     AttnTileArgs ta;
@@ -1181,24 +1198,44 @@ tern_status tern_attention(const tern_attention_args* args, tern_stream_t stream
     if ((s = make_heads_map(&ta.tq, q, &ta.q_h, &ta.q_b)) != TERN_OK || (s = make_heads_map(&ta.tk, k, &ta.k_h, &ta.k_b)) != TERN_OK ||
         (s = make_heads_map(&ta.tv, v, &ta.v_h, &ta.v_b)) != TERN_OK)
       return s;
-    if (tile_units > INT32_MAX) return fail(TERN_ERR_UNSUPPORTED_SHAPE, "attention: too many query rows");
-    ta.pairs = int(pairs);
-    ta.units = int(tile_units);
+    if (c.tile_units > INT32_MAX) return fail(TERN_ERR_UNSUPPORTED_SHAPE, "attention: too many query rows");
+    ta.pairs = int(c.pairs);
+    ta.units = int(c.tile_units);
     ta.ctas = ds->sms;
-    ta.splits = tile_splits;
+    ta.splits = c.ctas;
     ta.o_sectors = aligned(t.o, 32) && t.D % 16 == 0 && (t.B <= 1 || t.o_b % 16 == 0) && (t.Lq <= 1 || t.o_l % 16 == 0) &&
                    (t.H <= 1 || t.o_h % 16 == 0);
-    ta.by_pairs = div_by(unsigned(pairs));
+    ta.by_pairs = div_by(unsigned(c.pairs));
     ta.by_heads = div_by(unsigned(t.H));
     ta.by_group = div_by(unsigned(t.H / t.Hkv));
     // Some warps wait for others through whole units: the time of a launch
     // (1.5 us a key tile; 8 allowed) comes on top of the limit.
-    const double launch_ns = std::min(8000. * double(rounds) * double(tiles), 1e18);
+    const double launch_ns = std::min(8000. * double(c.rounds) * double(c.tiles), 1e18);
     ta.wait_limit_ns = std::min<unsigned long long>(g_wait_limit_ns.load(), 1ull << 60) + (unsigned long long)(launch_ns);
     ta.status = ds->status;
     e = launch_attention_tile(ta, reinterpret_cast<cudaStream_t>(stream));
   }
   if (e != cudaSuccess) return cuda_fail(e, "attention launch");
+  return TERN_OK;
+}
+
+tern_status tern_attention_plan(const tern_attention_args* args, int sms, int* kernel, int* ctas) {
+  if (!args || !kernel || !ctas) return fail(TERN_ERR_INVALID_ARG, "null args, kernel or ctas");
+  const tern_attention_args& t = *args;
+  tern_status s;
+  if ((s = check_attention_sizes(t)) != TERN_OK) return s;
+  *kernel = TERN_ATTENTION_NONE;
+  *ctas = 0;
+  if (t.B == 0 || t.Lq == 0 || t.H == 0) return TERN_OK;
+  if (sms <= 0) {
+    int dev;
+    DeviceState* ds;
+    if ((s = current_device(&dev, &ds)) != TERN_OK) return s;
+    sms = ds->sms;
+  }
+  const AttnChoice c = choose_attention(t, sms);
+  *kernel = c.rows ? TERN_ATTENTION_ROWS : TERN_ATTENTION_TILES;
+  *ctas = c.ctas;
   return TERN_OK;
 }
 

@@ -27,7 +27,7 @@ EXPORTED = ("tern_packed_bytes", "tern_quantize_pack", "tern_linear", "tern_line
             "tern_linear_act", "tern_linear_epilogue", "tern_linear_batch", "tern_linear_batch_act",
             "tern_linear_batch_epilogue", "tern_linear_strided", "tern_linear_batch_strided",
             "tern_adaln_modulate", "tern_quantize_act_e4m3", "tern_linear_e4m3",
-            "tern_rope_table", "tern_rope", "tern_attention", "tern_gated_residual_norm",
+            "tern_rope_table", "tern_rope", "tern_attention", "tern_attention_plan", "tern_gated_residual_norm",
             "tern_dequantize", "tern_get_device_status", "tern_set_wait_limit_ns",
             "tern_selftest_wait_timeout", "tern_status_string", "tern_last_error")
 
@@ -95,6 +95,10 @@ _RESIDUAL_NORM = struct.Struct("4P6qfiPfPiiPfPPqq")
 ACT_NONE = 0       # tern_act values
 ACT_GELU_TANH = 1
 
+ATTENTION_NONE = 0  # tern_attention_kernel values
+ATTENTION_ROWS = 1
+ATTENTION_TILES = 2
+
 NORM_NONE = 0      # tern_norm values
 NORM_RMS = 1
 NORM_LAYER = 2
@@ -149,6 +153,8 @@ def lib() -> ctypes.CDLL:
         L.tern_rope.restype = st
         L.tern_attention.argtypes = [vp, vp]
         L.tern_attention.restype = st
+        L.tern_attention_plan.argtypes = [vp, ctypes.c_int, vp, vp]
+        L.tern_attention_plan.restype = st
         L.tern_gated_residual_norm.argtypes = [vp, vp]
         L.tern_gated_residual_norm.restype = st
         L.tern_dequantize.argtypes = [vp, vp, i64, i64, vp, vp]
@@ -579,6 +585,19 @@ def attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, scale: Optional
         _ATTENTION.pack(q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(), B, Lq, Lk, H, Hkv, D, *sq[:3], *sk[:3],
                         *sv[:3], *so[:3], D ** -0.5 if scale is None else scale, lens, mask, mask_ld), raw))
     return out
+
+
+def attention_plan(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, sms: int = 0):
+    """tern_attention_plan: (ATTENTION_* kernel, CTAs that share the keys of a
+    unit) that `attention` takes for tensors of these shapes and strides (on any
+    device) on a GPU of `sms` SMs (0: the current one)."""
+    q, k, v = (t if t.dim() == 4 else t[None] for t in (q, k, v))
+    (B, Lq, H, D), (Lk, Hkv) = q.shape, k.shape[1:3]
+    args = _ATTENTION.pack(0, 0, 0, 0, B, Lq, Lk, H, Hkv, D, *q.stride()[:3], *k.stride()[:3], *v.stride()[:3], 0, 0, 0, 1.0,
+                           0, 0, 0)
+    kernel, ctas = ctypes.c_int(), ctypes.c_int()
+    _check(lib().tern_attention_plan(args, sms, ctypes.byref(kernel), ctypes.byref(ctas)))
+    return kernel.value, ctas.value
 
 
 def gated_residual_norm(x: torch.Tensor, o: torch.Tensor, *, gate: Optional[torch.Tensor] = None,

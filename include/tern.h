@@ -448,6 +448,19 @@ typedef struct {
 
 TERN_API tern_status tern_attention(const tern_attention_args* args, tern_stream_t stream);
 
+/* The two kernels of tern_attention. */
+typedef enum {
+  TERN_ATTENTION_NONE = 0, /* nothing to do */
+  TERN_ATTENTION_ROWS = 1, /* 16 query rows of a key-value head at a time */
+  TERN_ATTENTION_TILES = 2 /* 256 queries of a head at a time, tcgen05 */
+} tern_attention_kernel;
+
+/* Which of them tern_attention launches for the sizes and strides in args
+ * (pointers and the scale are not looked at) on a device of `sms` SMs (sms <= 0: the
+ * current device), and how many CTAs share the keys of each unit of its work.
+ * Host only. */
+TERN_API tern_status tern_attention_plan(const tern_attention_args* args, int sms, int* kernel, int* ctas);
+
 /* Normalisation of a row v of K channels (tern_gated_residual_norm). */
 typedef enum {
   TERN_NORM_NONE = 0,

@@ -253,3 +253,43 @@ def test_binding_refuses_what_does_not_fit():
 def test_binding_refuses_tensors_that_are_not_on_the_current_gpu(call):
     with pytest.raises(ValueError, match="current CUDA device"):
         call()
+
+
+# -------------------------------------------------- which kernel attention takes
+def test_attention_plan_refuses_and_answers_without_a_gpu(L):
+    def plan(sms=148, **kw):
+        d = dict(B=2, Lq=16, Lk=32, H=4, Hkv=2, D=64, q_l=256, k_l=128, v_l=128)
+        d.update(kw)
+        a = tern.AttentionArgs(**d)
+        kernel, ctas = ctypes.c_int(-7), ctypes.c_int(-7)
+        s = L.tern_attention_plan(ctypes.byref(a), sms, ctypes.byref(kernel), ctypes.byref(ctas))
+        return (kernel.value, ctas.value) if s == OK else s
+    n = ctypes.c_int()
+    assert L.tern_attention_plan(None, 148, ctypes.byref(n), ctypes.byref(n)) == INVALID
+    assert L.tern_attention_plan(ctypes.byref(tern.AttentionArgs()), 148, None, ctypes.byref(n)) == INVALID
+    assert plan(Lq=-1) == INVALID and plan(D=68) == SHAPE and plan(Hkv=3) == SHAPE and plan(Lk=1 << 30) == SHAPE
+    for empty in ("B", "Lq", "H"):
+        assert plan(**{empty: 0}) == (tern.ATTENTION_NONE, 0)
+    assert plan(Lk=0)[0] == tern.ATTENTION_ROWS
+    big = dict(B=1, Lq=4096, Lk=512, H=24, Hkv=24, D=128)
+    assert plan(**big) == (tern.ATTENTION_TILES, 1)
+    assert plan(**big, k_l=0)[0] == tern.ATTENTION_ROWS and plan(**big, q_l=0)[0] == tern.ATTENTION_ROWS
+    assert plan(B=1, Lq=256, Lk=16384, H=8, Hkv=8, D=128) == (tern.ATTENTION_TILES, 8)
+    assert plan(B=1, Lq=1, Lk=512, H=24, Hkv=24, D=128)[0] == tern.ATTENTION_ROWS
+    q, k = torch.empty(1, 256, 8, 128, device="meta"), torch.empty(1, 16384, 8, 128, device="meta")
+    assert tern.attention_plan(q, k, k, sms=148) == tern.attention_plan(q[0], k[0], k[0], sms=148) == (tern.ATTENTION_TILES, 8)
+
+
+def test_a_lost_remainder_of_the_probabilities_shows():
+    """The bar that the row kernel is held to: fp64 attention whose
+    probabilities are rounded to bf16 once is outside it."""
+    g = torch.Generator().manual_seed(5)
+    q, k, v = ((torch.randn(1, n, 4, 64, generator=g) * s).to(torch.bfloat16).double() for n, s in ((1, 1.4), (17, 1.4), (17, 1.0)))
+    want, av, big = ref.attention(q.numpy(), k.numpy(), v.numpy(), 0.125)
+    z = torch.einsum("bqhd,bkhd->bhqk", q, k) * 0.125
+    p = torch.exp(z - z.amax(-1, keepdim=True))
+    total = p.sum(-1, keepdim=True)
+    for step, inside in ((ref.BF16 ** 2, False), (ref.BF16, True)):
+        o = torch.einsum("bhqk,bkhd->bqhd", p.to(torch.bfloat16).double() / total, v).to(torch.bfloat16).double().numpy()
+        e = ref.attention_bound(q.numpy(), k.numpy(), av, big, step)
+        assert bool((np.abs(o - want) <= ref.BF16 * (np.abs(want) + e) + e).all()) == inside

@@ -1,0 +1,160 @@
+"""tern_attention by the kernel and the cluster size that a call takes, on the
+GPU against the fp64 oracle: each test asks tern_attention_plan where its
+sizes go and says so, so that a change of the rule cannot lead it elsewhere.
+
+Bars.  Tiles: the fp32 bound that the oracle derives with the probabilities
+rounded to bf16 once (2^-8 relative).  Rows: the probabilities enter as two
+bf16, value and remainder, so 2^-8 of 2^-8 is left.  Then one rounding of the
+output.
+"""
+from __future__ import annotations
+
+import numpy as np
+import pytest
+import torch
+
+from bit_post_quantised_b200 import tern
+from oracle import block_ops as ref
+
+pytestmark = pytest.mark.gpu
+ROWS, TILES = tern.ATTENTION_ROWS, tern.ATTENTION_TILES
+
+
+def rand(shape, seed, std=1.0):
+    g = torch.Generator().manual_seed(seed)
+    return (torch.randn(shape, generator=g) * std).to(torch.bfloat16)
+
+
+def inputs(B, Lq, Lk, H, Hkv, D, seed=0, std=1.4):
+    s = seed + B + 3 * Lq + 5 * Lk + 7 * H + D
+    return (rand((B, Lq, H, D), s, std).cuda(), rand((B, Lk, Hkv, D), s + 1, std).cuda(),
+            rand((B, Lk, Hkv, D), s + 2).cuda())
+
+
+def f64(t):
+    return t.detach().cpu().double().numpy()
+
+
+def close(o, q, k, v, kernel, scale=None, valid=None):
+    qd, kd, vd = f64(q), f64(k), f64(v)
+    want, av, big = ref.attention(qd, kd, vd, qd.shape[-1] ** -0.5 if scale is None else scale, None,
+                                  None if valid is None else valid.numpy())
+    e = ref.attention_bound(qd, kd, av, big, ref.BF16 if kernel == TILES else ref.BF16 ** 2)
+    got = f64(o)
+    bad = ~(np.abs(got - want) <= ref.BF16 * (np.abs(want) + e) + e)
+    assert not bad.any(), f"{int(bad.sum())} of {bad.size} out of tolerance, first at {np.argwhere(bad)[0]}"
+    assert tern.device_status() == 0
+
+
+# Sizes, and where they go on a B200 (148 SMs).
+EIGHT = [(1, 256, 16384, 4, 4, 128), (1, 256, 16384, 8, 8, 64), (1, 300, 8192, 4, 2, 128), (1, 129, 9001, 5, 5, 96),
+         (2, 250, 16001, 3, 3, 40)]
+ONE = [(1, 300, 200, 24, 24, 128), (1, 300, 200, 24, 24, 64), (1, 1700, 200, 24, 8, 96)]
+SHARED = [(1, 300, 4000, 4, 4, 128), (1, 300, 4000, 4, 4, 64), (1, 1000, 1500, 5, 5, 128)]
+FEW = [(1, 1, 512, 24, 24, 128), (2, 1, 17, 6, 2, 64), (3, 17, 531, 16, 4, 64), (1, 40, 700, 8, 4, 128), (1, 1, 5000, 2, 2, 64),
+       (2, 129, 257, 3, 3, 128), (1, 255, 64, 2, 1, 40), (1, 7, 2, 4, 4, 64), (1, 3, 9000, 8, 1, 72)]
+
+
+@pytest.mark.parametrize("B,Lq,Lk,H,Hkv,D", FEW)
+@pytest.mark.parametrize("masked", [False, True])
+def test_rows_lose_nothing_but_the_last_rounding(B, Lq, Lk, H, Hkv, D, masked):
+    q, k, v = inputs(B, Lq, Lk, H, Hkv, D, seed=31)
+    assert tern.attention_plan(q, k, v)[0] == ROWS
+    if not masked:
+        return close(tern.attention(q, k, v), q, k, v, ROWS)
+    m = torch.rand(B, Lk, generator=torch.Generator().manual_seed(Lk)) < 0.7
+    kd, vd = k.clone(), v.clone()
+    kd[(~m).cuda()] = float("inf")
+    vd[(~m).cuda()] = float("nan")
+    close(tern.attention(q, kd, vd, key_mask=m.cuda()), q, k, v, ROWS, valid=m)
+
+
+@pytest.mark.parametrize("B,Lq,Lk,H,Hkv,D", EIGHT)
+@pytest.mark.parametrize("kind", ["none", "len", "short", "mask"])
+def test_eight_ctas_share_the_keys(B, Lq, Lk, H, Hkv, D, kind):
+    """Whole lengths, one that ends inside the sixth share, one that leaves
+    seven shares without a key, a mask that empties the shares in the middle
+    and (with two entries) an entry without a key; rows behind the last query
+    as they were; the same bits every time."""
+    q, k, v = inputs(B, Lq, Lk, H, Hkv, D, seed=41)
+    assert tern.attention_plan(q, k, v) == (TILES, 8)
+    n = m = None
+    valid = torch.ones(B, Lk, dtype=torch.bool)
+    if kind in ("len", "short"):
+        n = torch.tensor([Lk * 11 // 16 + 3 if kind == "len" else 77, 0][:B], dtype=torch.int32)
+        valid &= torch.arange(Lk)[None] < n[:, None]
+    elif kind == "mask":
+        m = torch.rand(B, Lk, generator=torch.Generator().manual_seed(Lq)) < 0.5
+        m[0, Lk // 4:Lk // 2 + 300] = False
+        m[1:] = False
+        valid &= m
+    bad = (~valid).cuda()
+    kd, vd = k.clone(), v.clone()
+    kd[bad] = float("nan")
+    vd[bad] = float("inf")
+    n, m = (None if n is None else n.cuda()), (None if m is None else m.cuda())
+    out = torch.full((B, Lq + 2, H, D), 5.0, dtype=torch.bfloat16, device="cuda")
+    o = tern.attention(q, kd, vd, kv_len=n, key_mask=m, out=out[:, :Lq])
+    close(o, q, k, v, TILES, valid=valid)
+    assert (o[~valid.any(1)] == 0).all() and (out[:, Lq:] == 5).all()
+    for _ in range(3):
+        assert torch.equal(tern.attention(q, kd, vd, kv_len=n, key_mask=m), o)
+
+
+def test_eight_ctas_on_two_streams_and_in_a_graph():
+    a, b = inputs(*EIGHT[0]), inputs(*EIGHT[1])
+    assert tern.attention_plan(*a) == (TILES, 8) and tern.attention_plan(*b) == (TILES, 8)
+    wa, wb = tern.attention(*a), tern.attention(*b)
+    s, r = torch.cuda.Stream(), torch.cuda.Stream()
+    for st in (s, r):
+        st.wait_stream(torch.cuda.current_stream())
+    oa = [tern.attention(*a, stream=s) for _ in range(6)]
+    ob = [tern.attention(*b, stream=r) for _ in range(6)]
+    torch.cuda.synchronize()
+    assert all(torch.equal(o, wa) for o in oa) and all(torch.equal(o, wb) for o in ob)
+    out = torch.empty_like(wa)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        tern.attention(*a, out=out)
+    a[0].copy_(rand(a[0].shape, 5))
+    g.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(out, tern.attention(*a))
+    close(out, *a, TILES)
+
+
+CASES = [(s, ROWS, None) for s in FEW if s[1] > 1] + [(s, TILES, 1) for s in ONE] + [(s, TILES, None) for s in SHARED] + [
+    (s, TILES, 8) for s in EIGHT[:2]]
+
+
+def goes(q, k, v, kernel, ctas):
+    got = tern.attention_plan(q, k, v)
+    assert got[0] == kernel and (ctas is None or got[1] == ctas), got
+    assert ctas is not None or kernel == ROWS or got[1] > 1, got
+
+
+@pytest.mark.parametrize("size,kernel,ctas", CASES)
+def test_a_nan_score_stays_in_its_row(size, kernel, ctas):
+    q, k, v = inputs(*size)
+    goes(q, k, v, kernel, ctas)
+    want = tern.attention(q, k, v)
+    q[0, 1, 0, 3] = float("nan")
+    got = tern.attention(q, k, v)
+    assert torch.isnan(got[0, 1, 0]).all()
+    got[0, 1, 0] = want[0, 1, 0]
+    assert torch.equal(got, want)
+
+
+@pytest.mark.parametrize("size,kernel,ctas", [((1, 4, 300, 1, 1, 64), ROWS, None), ((1, 300, 300, 24, 24, 128), TILES, 1),
+                                              ((1, 300, 300, 24, 24, 64), TILES, 1), ((1, 1000, 300, 24, 24, 128), TILES, 1)])
+def test_keys_behind_32_bit_offsets(size, kernel, ctas):
+    """Keys and values whose tokens span more than 2^32 bytes of one buffer."""
+    _, Lq, Lk, H, _, D = size
+    ld = 1 << 24
+    big = torch.empty(Lk * ld, dtype=torch.bfloat16, device="cuda")
+    k, v = (big[i * H * D:].as_strided((1, Lk, H, D), (0, ld, D, 1)) for i in range(2))
+    q, kk, vv = inputs(*size)
+    goes(q, k, v, kernel, ctas)
+    k.copy_(kk)
+    v.copy_(vv)
+    assert torch.equal(tern.attention(q, k, v), tern.attention(q, kk, vv))
