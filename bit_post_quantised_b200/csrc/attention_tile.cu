@@ -437,7 +437,18 @@ __global__ void __launch_bounds__(kThreads, 1) attention_tile_kernel(const __gri
             }
           }
         }
-        const float base = m == -INFINITY ? 0.f : -m * sl;
+        float base = m == -INFINITY ? 0.f : -m * sl;
+        // The multiply-add below rounds m * sl but not v * sl: a factor of up to
+        // 2^(2^-24 |m * sl|) common to the row's probabilities, which would
+        // overflow where scores are that far from zero.  There the reference is
+        // taken off first.  (The test costs 4608 x 4608 x 24 heads 1 %.)
+        if (fabsf(base) > 1048576.f) {
+          base = 0.f;
+#pragma unroll
+          for (int c = 0; c < 4; ++c)
+#pragma unroll
+            for (int e = 0; e < 32; ++e) v[c][e] = __float_as_uint(__uint_as_float(v[c][e]) - m);
+        }
         const float2 base2 = make_float2(base, base);
         float2 acc[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll
@@ -461,10 +472,9 @@ __global__ void __launch_bounds__(kThreads, 1) attention_tile_kernel(const __gri
         }
         acc[0] = add2(acc[0], acc[1]);
         sum += acc[0].x + acc[0].y;
-        // The maximum itself overflowed in log2 units: against -inf every probability was 0.
-        if (base == -INFINITY) sum = NAN;
       }
       if (!ok) break;
+      if (m * sl == INFINITY) sum = NAN;  // the maximum itself is not finite in log2 units
       if (SPLIT || x.n == 0) continue;
       // The rows' sums to the output warps, once they are through with the unit before.
       ok = __all_sync(0xffffffffu, bar_wait(smem_u32(&o_free[i]), fp, lim, st));

@@ -145,6 +145,29 @@ def test_a_nan_score_stays_in_its_row(size, kernel, ctas):
     assert torch.equal(got, want)
 
 
+def lone(q, k, key, value):
+    """Query 1 and `key` meet in one channel, with the product |value| * value;
+    every other score of either is zero."""
+    q[0, 1], k[0, key] = 0.0, 0.0
+    q[0, :, :, 3] = 0.0
+    k[0, :, :, 3] = 0.0
+    q[0, 1, :, 3] = abs(value)
+    k[0, key, :, 3] = value
+
+
+@pytest.mark.parametrize("size,kernel,ctas", CASES)
+def test_a_scaled_score_that_overflows_gives_nan_rows(size, kernel, ctas):
+    """2^60 * 2^60 * 2^40 = 2^160: not in fp32.  The other rows are finite."""
+    q, k, v = inputs(*size)
+    goes(q, k, v, kernel, ctas)
+    lone(q, k, size[2] // 2, 2.0 ** 60)
+    got = tern.attention(q, k, v, scale=2.0 ** 40)
+    assert torch.isnan(got[0, 1]).all()
+    rest = torch.arange(size[1], device="cuda") != 1
+    assert torch.isfinite(got[0, rest]).all() and torch.isfinite(got[1:]).all()
+    assert tern.device_status() == 0
+
+
 @pytest.mark.parametrize("size,kernel,ctas", [((1, 4, 300, 1, 1, 64), ROWS, None), ((1, 300, 300, 24, 24, 128), TILES, 1),
                                               ((1, 300, 300, 24, 24, 64), TILES, 1), ((1, 1000, 300, 24, 24, 128), TILES, 1)])
 def test_keys_behind_32_bit_offsets(size, kernel, ctas):
@@ -158,3 +181,30 @@ def test_keys_behind_32_bit_offsets(size, kernel, ctas):
     k.copy_(kk)
     v.copy_(vv)
     assert torch.equal(tern.attention(q, k, v), tern.attention(q, kk, vv))
+
+
+@pytest.mark.parametrize("size,kernel,ctas", CASES)
+@pytest.mark.parametrize("scale", [2.0 ** 16, 2.0 ** 27, 2.0 ** 100])
+def test_scaled_scores_far_from_zero(size, kernel, ctas, scale):
+    """A scale by which only the row's highest score counts (or several, where
+    they are equal): q and k hold small whole numbers, so that scores are
+    exact in fp32 and ties are ties."""
+    B, Lq, Lk, H, Hkv, D = size
+    g = torch.Generator().manual_seed(Lk + H)
+    q = torch.randint(-3, 4, (B, Lq, H, D), generator=g).to(torch.bfloat16).cuda()
+    k = torch.randint(-3, 4, (B, Lk, Hkv, D), generator=g).to(torch.bfloat16).cuda()
+    v = rand((B, Lk, Hkv, D), 3).cuda()
+    goes(q, k, v, kernel, ctas)
+    got = f64(tern.attention(q, k, v, scale=scale))
+    G = H // Hkv
+    qd, kd, vd = q.double().cpu(), k.double().cpu().repeat_interleave(G, 2), v.double().cpu().repeat_interleave(G, 2)
+    s = torch.einsum("bqhd,bkhd->bhqk", qd, kd)
+    p = (s == s.amax(-1, keepdim=True)).double()
+    p /= p.sum(-1, keepdim=True)
+    want = torch.einsum("bhqk,bkhd->bqhd", p, vd).numpy()
+    av = torch.einsum("bhqk,bkhd->bqhd", p, vd.abs()).numpy()
+    # Equal scores have equal probabilities, exactly 1 against their maximum or 2^(up to 8 and its
+    # rounding, 2^-20) against an older reference, rounded alike: the factor's bf16 rounding stays.
+    e = ((ref.BF16 if kernel == TILES else ref.BF16 ** 2) + 2.0 ** -20 + (Lk / 4 + 16) * ref.F32) * av
+    assert np.all(np.abs(got - want) <= ref.BF16 * (np.abs(want) + e) + e)
+    assert tern.device_status() == 0
