@@ -24,7 +24,9 @@
 // remainder): the extra product is free under the memory bound and leaves
 // only the final rounding.  Masked keys have their score replaced (not added
 // to) and their value row zeroed, so whatever they hold is not seen; a row
-// without a valid key gives zeros.
+// without a valid key gives zeros.  Where the valid keys' scores are all -inf or
+// NaN the maximum becomes -FLT_MAX, to tell the row from one without a key: it
+// has nothing to divide by, or a sum that is NaN, and gives NaN.
 //
 // The ring is sized for two CTAs an SM, which also lets eight clusters of 16
 // be resident.  Many heads are bound by memory (64 x 1 query, 4096 keys, 8 heads:
@@ -37,6 +39,8 @@
 // Join: the four warps of a CTA combine their (max, sum, output) through
 // shared memory, then the CTAs of the cluster through distributed shared
 // memory, each CTA writing a slice of the rows: one launch, no workspace.
+#include <cfloat>
+
 #include "internal.h"
 #include "kernel_common.cuh"
 #include "ptx.cuh"
@@ -145,6 +149,7 @@ __global__ void __launch_bounds__(kWarps * 32, 2) attention_rows_kernel(const __
     }
   }
   float m[2] = {-INFINITY, -INFINITY}, sum[2] = {0.f, 0.f};
+  bool seen = false;  // a valid key
   float o[8 * NC][4];
 #pragma unroll
   for (int j = 0; j < 8 * NC; ++j) o[j][0] = o[j][1] = o[j][2] = o[j][3] = 0.f;
@@ -199,7 +204,10 @@ __global__ void __launch_bounds__(kWarps * 32, 2) attention_rows_kernel(const __
         for (int e = 0; e < 2; ++e) {
           const int key = blk * kKeys + nt * 8 + 2 * t + e;
           ok[nt][e] = key < len && (!mask || mask[key]);
+          seen |= ok[nt][e];
         }
+    } else {
+      seen = true;
     }
     asm volatile("cp.async.wait_group %0;" ::"n"(ST - 2) : "memory");
     __syncwarp();  // every lane's copies are in, and its reads of the stage refilled next are done
@@ -300,8 +308,10 @@ __global__ void __launch_bounds__(kWarps * 32, 2) attention_rows_kernel(const __
   // ---- join, over the rings once every warp is through with its own
   asm volatile("cp.async.wait_group 0;" ::: "memory");
   __syncthreads();
+  seen = __any_sync(0xffffffffu, seen);  // the keys are the same for every row
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
+    if (seen && m[h] == -INFINITY) m[h] = -FLT_MAX;
     sum[h] += __shfl_xor_sync(0xffffffffu, sum[h], 1);
     sum[h] += __shfl_xor_sync(0xffffffffu, sum[h], 2);
     if (t == 0) {
@@ -329,8 +339,7 @@ __global__ void __launch_bounds__(kWarps * 32, 2) attention_rows_kernel(const __
     for (int w = 0; w < kWarps; ++w) {
       const float mw = sm_ml[w][r][0];
       f[w] = mw == -INFINITY ? 0.f : exp2_fast(mw - top);
-      // A row whose scores are NaN has no maximum; its sum is NaN and stays so.
-      total += sm_ml[w][r][1] * (mw == -INFINITY ? 1.f : f[w]);
+      total = fmaf(sm_ml[w][r][1], f[w], total);
     }
     if (part == 0) cta_ml[r][0] = top, cta_ml[r][1] = total;
     for (int d = part * 2; d < DP; d += 16) {
@@ -353,7 +362,7 @@ __global__ void __launch_bounds__(kWarps * 32, 2) attention_rows_kernel(const __
     if (row >= R || d >= a.D) continue;
     float x = 0.f, y = 0.f, total = 0.f, top = -INFINITY;
     if (splits == 1) {
-      total = cta_ml[r][1];
+      top = cta_ml[r][0], total = cta_ml[r][1];
       x = cta_o[r][d], y = cta_o[r][d + 1];
     } else {
       for (int s = 0; s < splits; ++s) top = fmaxf(top, ld_cluster_f2(mapa_shared(ml0 + r * 8, s)).x);
@@ -361,12 +370,12 @@ __global__ void __launch_bounds__(kWarps * 32, 2) attention_rows_kernel(const __
         const float2 ml = ld_cluster_f2(mapa_shared(ml0 + r * 8, s));
         const float2 v = ld_cluster_f2(mapa_shared(o0 + (r * DP + d) * 4, s));
         const float f = ml.x == -INFINITY ? 0.f : exp2_fast(ml.x - top);
-        total += ml.y * (ml.x == -INFINITY ? 1.f : f);
+        total = fmaf(ml.y, f, total);
         x = fmaf(v.x, f, x);
         y = fmaf(v.y, f, y);
       }
     }
-    const float inv = total == 0.f ? 0.f : 1.f / total;
+    const float inv = top == -INFINITY ? 0.f : 1.f / total;
     uint32_t w;
     asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(w) : "f"(y * inv), "f"(x * inv));
     *reinterpret_cast<uint32_t*>(a.o + b * a.o_b + (row / G) * a.o_l + (hk * G + row % G) * a.o_h + d) = w;

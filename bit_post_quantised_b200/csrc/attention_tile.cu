@@ -55,7 +55,9 @@
 // Masked keys: S is replaced by -inf there (whatever it holds) and their V
 // rows are overwritten with zeros in shared memory, since 0 * NaN would reach
 // O.  Key tiles past kv_len are not loaded.  A row without a valid key gives
-// zeros.
+// zeros; one with valid keys whose highest score is not finite, NaN.
+#include <cfloat>
+
 #include "internal.h"
 #include "kernel_common.cuh"
 #include "ptx.cuh"
@@ -266,7 +268,7 @@ __device__ __forceinline__ void join(uint32_t ring, int stats, int row_floats, i
       for (int e = 0; e < 8; ++e) acc[e] = 0.f;
 #pragma unroll
       for (int p = 0; p < NS; ++p) {
-        // Without a valid key there O was not written; a NaN score's sum is NaN, and the row with it.
+        // Without a key there O was not written.
         const bool none = ms[n][p].x == -INFINITY;
         const float f = none ? 1.f : exp2_fast((ms[n][p].x - top) * sl);
         total = fmaf(ms[n][p].y, f, total);
@@ -275,7 +277,7 @@ __device__ __forceinline__ void join(uint32_t ring, int stats, int row_floats, i
 #pragma unroll
         for (int e = 0; e < 8; ++e) acc[e] = none ? acc[e] : fmaf(w[e], f, acc[e]);
       }
-      const float inv = total == 0.f ? 0.f : 1.f / total;
+      const float inv = top == -INFINITY ? 0.f : isinf(top * sl) ? NAN : 1.f / total;
       if (row < rows && ch < a.D)
         *reinterpret_cast<uint4*>(o + (long long)row * a.o_l + ch) =
             make_uint4(pack2(acc[0] * inv, acc[1] * inv), pack2(acc[2] * inv, acc[3] * inv), pack2(acc[4] * inv, acc[5] * inv),
@@ -364,7 +366,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_tile_kernel(const __gri
     uint32_t sp = 0, fp = 1;  // phases of s_full and o_free
     int mt = 0;  // key tiles so far (the slot and phase of the validity words)
     float m = -INFINITY, sum = 0.f;
-    bool ok = true;
+    bool ok = true, seen = false;  // a valid key in the unit
     for (int u = u0; u < units && ok; u += ustep) {
       const Unit x = unit_of<MASK, SPLIT>(t, u);
       if (i >= x.nq) {
@@ -378,6 +380,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_tile_kernel(const __gri
         continue;
       }
       m = -INFINITY, sum = 0.f;
+      seen = !MASK && x.n > 0;
       for (int j = 0; j < x.n; ++j) {
         ok = __all_sync(0xffffffffu, bar_wait(smem_u32(&s_full[i]), sp, lim, st));
         if (!ok) break;
@@ -395,6 +398,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_tile_kernel(const __gri
             if (!ok) break;
             const uint4 mw = *reinterpret_cast<const uint4*>(m_words[ms]);
             w[0] = mw.x, w[1] = mw.y, w[2] = mw.z, w[3] = mw.w;
+            seen |= (mw.x | mw.y | mw.z | mw.w) != 0u;
             __syncwarp();
             if (lane == 0) mbar_arrive(smem_u32(&m_empty[ms]));
             ++mt;
@@ -474,13 +478,16 @@ __global__ void __launch_bounds__(kThreads, 1) attention_tile_kernel(const __gri
         sum += acc[0].x + acc[0].y;
       }
       if (!ok) break;
-      if (m * sl == INFINITY) sum = NAN;  // the maximum itself is not finite in log2 units
+      if constexpr (SPLIT) {
+        // Only NaN and -inf among valid keys: told from no key by a maximum that is finite.
+        if (seen && m == -INFINITY) m = -FLT_MAX;
+      }
       if (SPLIT || x.n == 0) continue;
       // The rows' sums to the output warps, once they are through with the unit before.
       ok = __all_sync(0xffffffffu, bar_wait(smem_u32(&o_free[i]), fp, lim, st));
       if (!ok) break;
       fp ^= 1;
-      inv_sum[i][(warp & 3) * 32 + lane] = sum == 0.f ? 0.f : 1.f / sum;
+      inv_sum[i][(warp & 3) * 32 + lane] = !seen ? 0.f : isinf(m * sl) ? NAN : 1.f / sum;
       __syncwarp();
       if (lane == 0) mbar_arrive(smem_u32(&sum_full[i]));
     }

@@ -421,7 +421,8 @@ TERN_API tern_status tern_rope(const tern_rope_tensor* tensors, int count, int64
  * h' = h / (H / Hkv), over the valid keys j < kv_len[b] with key_mask[b, j]
  * != 0.  A batch entry without a valid key gives zeros.  What masked keys and
  * values hold (infinities and NaN too) does not reach the output; scores that
- * are NaN, or infinite at their row's maximum, give NaN rows.
+ * are NaN, or infinite (of either sign, in fp32 and with the scale) at their
+ * row's maximum, give NaN rows.
  *   q, o      [B, Lq, H, D];  k, v  [B, Lk, Hkv, D]; channels are adjacent.
  *   kv_len    [B] int32 device memory or NULL (all Lk); clamped to [0, Lk].
  *   key_mask  [B, Lk] bytes device memory, rows mask_ld apart, or NULL.

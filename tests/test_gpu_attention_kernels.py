@@ -208,3 +208,85 @@ def test_scaled_scores_far_from_zero(size, kernel, ctas, scale):
     e = ((ref.BF16 if kernel == TILES else ref.BF16 ** 2) + 2.0 ** -20 + (Lk / 4 + 16) * ref.F32) * av
     assert np.all(np.abs(got - want) <= ref.BF16 * (np.abs(want) + e) + e)
     assert tern.device_status() == 0
+
+
+def masked_like(q, k, v, gone, scale):
+    """fp64 attention of entry 0 without the keys `gone`."""
+    keep = ~gone.cpu()
+    return ref.attention(f64(q[:1]), f64(k[:1]), f64(v[:1]), scale, None, keep[None].numpy())
+
+
+@pytest.mark.parametrize("size,kernel,ctas", CASES)
+@pytest.mark.parametrize("raw", [True, False])
+def test_rows_whose_scores_are_all_minus_infinity(size, kernel, ctas, raw):
+    """Query 1's scores with every key are -inf, from an infinite channel or from
+    the scale (-2^60 * 2^60 * 2^40): NaN, as a maximum that is not finite gives.
+    The others' are as they are without that channel."""
+    B, Lq, Lk, H, Hkv, D = size
+    q, k, v = inputs(*size)
+    goes(q, k, v, kernel, ctas)
+    scale = D ** -0.5 if raw else 2.0 ** 40
+    q[0, :, :, 3] = 0.0
+    k[0, :, :, 3] = 1.0 if raw else -2.0 ** 60
+    if not raw:
+        q[0, 1] = 0.0
+    q[0, 1, :, 3] = float("-inf") if raw else 2.0 ** 60
+    got = tern.attention(q, k, v, scale=scale)
+    assert torch.isnan(got[0, 1]).all()
+    rest = torch.arange(Lq, device="cuda") != 1
+    assert torch.isfinite(got[0, rest]).all() and torch.isfinite(got[1:]).all()
+    if raw:
+        q[0, 1, :, 3] = 0.0
+        want = tern.attention(q, k, v, scale=scale)
+        assert torch.equal(got[0, rest], want[0, rest]) and torch.equal(got[1:], want[1:])
+
+
+@pytest.mark.parametrize("size,kernel,ctas", CASES)
+@pytest.mark.parametrize("raw", [True, False])
+@pytest.mark.parametrize("where", ["first", "last"])
+def test_keys_at_minus_infinity_before_and_behind_finite_ones(size, kernel, ctas, raw, where):
+    """Three quarters of the keys score -inf with every query, raw or by the
+    scale; the rest decide, as if those keys were not there."""
+    B, Lq, Lk, H, Hkv, D = size
+    if Lk < 8:
+        pytest.skip("no quarter")
+    q, k, v = inputs(*size)
+    goes(q, k, v, kernel, ctas)
+    gone = torch.arange(Lk, device="cuda") < Lk - Lk // 4
+    if where == "last":
+        gone = gone.flip(0)
+    scale = D ** -0.5 if raw else 2.0 ** 40
+    if not raw:  # 2^40 * 2^-20 * 2^-20 of the scores: ordinary sizes
+        q, k = q * 2.0 ** -20, k * 2.0 ** -20
+        q[0, :, :, 3], k[0, :, :, 3] = 2.0 ** 60, 0.0
+        k[0, gone, :, 3] = -2.0 ** 60
+    else:
+        q[0, :, :, 3], k[0, :, :, 3] = 1.0, 0.0
+        k[0, gone, :, 3] = float("-inf")
+    got = f64(tern.attention(q, k, v, scale=scale)[:1])
+    k[0, gone, :, 3] = 0.0
+    want, av, big = masked_like(q, k, v, gone, scale)
+    e = ref.attention_bound(f64(q[:1]), f64(k[:1]), av, big, ref.BF16 if kernel == TILES else ref.BF16 ** 2)
+    assert np.all(np.abs(got - want) <= ref.BF16 * (np.abs(want) + e) + e)
+
+
+@pytest.mark.parametrize("size,kernel,ctas", CASES)
+def test_minus_infinity_under_a_mask(size, kernel, ctas):
+    """The valid keys score -inf, the masked ones would not: NaN rows; an entry
+    without a valid key is zeros beside them."""
+    B, Lq, Lk, H, Hkv, D = size
+    if Lk < 8:
+        pytest.skip("no quarter")
+    q, k, v = inputs(2, *size[1:])
+    m = torch.zeros(2, Lk, dtype=torch.bool, device="cuda")
+    m[0, Lk // 2:Lk // 2 + Lk // 4] = True
+    q[0, :, :, 3], k[0, :, :, 3] = 1.0, 0.0
+    k[0, m[0], :, 3] = float("-inf")
+    got = tern.attention(q, k, v, key_mask=m)
+    assert torch.isnan(got[0]).all() and (got[1] == 0).all()
+    n = torch.tensor([Lk // 4, 0], dtype=torch.int32, device="cuda")
+    k[0, :, :, 3] = 0.0
+    k[0, :Lk // 4, :, 3] = float("-inf")
+    got = tern.attention(q, k, v, kv_len=n)
+    assert torch.isnan(got[0]).all() and (got[1] == 0).all()
+    assert tern.device_status() == 0
