@@ -183,7 +183,8 @@ cudaError_t launch_rope(const RopeArgs& a, bool halves, cudaStream_t stream) {
   // About 256 threads: a batch of heads for each, then further token rows.
   const int units = a.head_dim / 8, slots = 256 / units;
   const int ny = min(slots, (heads + kBatch - 1) / kBatch), nz = min(slots / ny, 64);
-  const dim3 grid(unsigned((a.rows + nz - 1) / nz), unsigned(count)), block(units, ny, nz);
+  // unsigned: rows may be next to 2^31
+  const dim3 grid((unsigned(a.rows) + unsigned(nz) - 1) / unsigned(nz), unsigned(count)), block(units, ny, nz);
   return halves ? launch_pdl(rope_kernel<true>, grid, block, 0, stream, 1, a)
                 : launch_pdl(rope_kernel<false>, grid, block, 0, stream, 1, a);
 }

@@ -1,0 +1,32 @@
+"""tern_rope and tern_rope_table at the ends of their documented ranges, on the GPU."""
+from __future__ import annotations
+
+import torch
+
+import pytest
+
+from bit_post_quantised_b200 import tern
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.mark.parametrize("rows", [2 ** 31 - 1, 2 ** 31 - 64])
+def test_rotation_of_as_many_rows_as_there_may_be(rows):
+    """One broadcast token for each of the last row counts below 2^31 (64 GB of
+    output): every row is the rotation of that token."""
+    D = 16
+    cs = tern.rope_table(torch.tensor([[0.75]], device="cuda"), (D,))
+    x = torch.randn(1, 1, 1, D, generator=torch.Generator().manual_seed(1)).to(torch.bfloat16).cuda()
+    want = tern.rope([x], cs)[0].view(D)
+    y = torch.empty(rows, 1, 1, D, dtype=torch.bfloat16, device="cuda")
+    try:
+        y[-1] = 0.0
+        tern.rope([x.expand(rows, 1, 1, D)], cs, outs=[y])
+        words = y.view(-1).view(torch.int64).view(rows, D // 4)
+        ref = want.view(torch.int64)
+        for at in range(0, rows, 1 << 27):
+            assert (words[at:at + (1 << 27)] == ref).all()
+    finally:
+        del y
+        words = None
+        torch.cuda.empty_cache()
