@@ -1046,6 +1046,9 @@ tern_status check_attention_sizes(const tern_attention_args& t) {
                 (long long)t.Hkv);
   if (t.Lq >= kMaxL || t.Lk >= kMaxL || t.B >= kMaxBH || t.H >= kMaxBH || t.B * t.H >= kMaxBH)
     return fail(TERN_ERR_UNSUPPORTED_SHAPE, "attention: Lq and Lk are below 2^30, B * H below 2^20");
+  // Either kernel's units then stay far below 2^31: 16 rows of a key-value head, 256 queries of a head.
+  if (t.B * t.H * t.Lq >= int64_t(1) << 34)
+    return fail(TERN_ERR_UNSUPPORTED_SHAPE, "attention: B * H * Lq is below 2^34");
   return TERN_OK;
 }
 
@@ -1181,8 +1184,6 @@ tern_status tern_attention(const tern_attention_args* args, tern_stream_t stream
   a.mask_ld = t.mask_ld;
   a.B = int(t.B), a.Lq = int(t.Lq), a.Lk = int(t.Lk), a.H = int(t.H), a.Hkv = int(t.Hkv), a.D = int(t.D);
   a.scale_log2 = scale_log2;
-  if ((t.Lq * (t.H / t.Hkv) + 15) / 16 * t.Hkv * t.B * 16 > INT32_MAX)
-    return fail(TERN_ERR_UNSUPPORTED_SHAPE, "attention: too many query rows");
   int dev;
   DeviceState* ds;
   tern_status s;
@@ -1198,7 +1199,6 @@ tern_status tern_attention(const tern_attention_args* args, tern_stream_t stream
     if ((s = make_heads_map(&ta.tq, q, &ta.q_h, &ta.q_b)) != TERN_OK || (s = make_heads_map(&ta.tk, k, &ta.k_h, &ta.k_b)) != TERN_OK ||
         (s = make_heads_map(&ta.tv, v, &ta.v_h, &ta.v_b)) != TERN_OK)
       return s;
-    if (c.tile_units > INT32_MAX) return fail(TERN_ERR_UNSUPPORTED_SHAPE, "attention: too many query rows");
     ta.pairs = int(c.pairs);
     ta.units = int(c.tile_units);
     ta.ctas = ds->sms;

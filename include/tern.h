@@ -426,8 +426,8 @@ TERN_API tern_status tern_rope(const tern_rope_tensor* tensors, int count, int64
  *   q, o      [B, Lq, H, D];  k, v  [B, Lk, Hkv, D]; channels are adjacent.
  *   kv_len    [B] int32 device memory or NULL (all Lk); clamped to [0, Lk].
  *   key_mask  [B, Lk] bytes device memory, rows mask_ld apart, or NULL.
- * H % Hkv == 0, D % 8 == 0, 8 <= D <= 128, Lq, Lk < 2^30 and B * H < 2^20
- * (TERN_ERR_UNSUPPORTED_SHAPE); pointers 16-byte aligned, strides multiples
+ * H % Hkv == 0, D % 8 == 0, 8 <= D <= 128, Lq, Lk < 2^30, B * H < 2^20 and
+ * B * H * Lq < 2^34 (TERN_ERR_UNSUPPORTED_SHAPE); pointers 16-byte aligned, strides multiples
  * of 8 below 2^38, 0 allowed in q, k and v (a broadcast); the elements of o
  * are distinct (strides as tern_rope's y) and o overlaps no input.  scale > 0
  * and below 2^127.  B, Lq or H == 0 is a no-op; Lk == 0 writes zeros (k and v may

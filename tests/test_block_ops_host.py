@@ -293,3 +293,14 @@ def test_a_lost_remainder_of_the_probabilities_shows():
         o = torch.einsum("bhqk,bkhd->bqhd", p.to(torch.bfloat16).double() / total, v).to(torch.bfloat16).double().numpy()
         e = ref.attention_bound(q.numpy(), k.numpy(), av, big, step)
         assert bool((np.abs(o - want) <= ref.BF16 * (np.abs(want) + e) + e).all()) == inside
+
+
+def test_attention_takes_as_many_query_rows_as_documented(L):
+    """B * H * Lq up to 2^34, whichever kernel they take."""
+    far = dict(k=F - 0x40000000, v=F - 0x20000000, B=1, H=8, Hkv=8, D=8, q_l=8, q_h=0, k_l=64, k_h=8, v_l=64, v_h=8, o_l=64, o_h=8,
+               o=F + (1 << 40))
+    if not torch.cuda.is_available():  # passes every check, up to the device query
+        assert _attn(L, **far, Lq=(1 << 28) + 5, Lk=3) in (-4, -6)
+    assert _attn(L, **far, Lq=(1 << 30) - 1, Lk=0, kv_len=1) == MISALIGNED  # refused for that alone
+    far.update(H=32, Hkv=32, o_l=256)
+    assert _attn(L, **far, Lq=1 << 29, Lk=3) == SHAPE

@@ -290,3 +290,29 @@ def test_minus_infinity_under_a_mask(size, kernel, ctas):
     got = tern.attention(q, k, v, kv_len=n)
     assert torch.isnan(got[0]).all() and (got[1] == 0).all()
     assert tern.device_status() == 0
+
+
+@pytest.mark.parametrize("Lk", [1, 3])
+def test_more_than_2_to_the_31_query_rows(Lk):
+    """2^28 + 5 queries of 8 heads of 8 channels (34 GB of output): with one key
+    every output is that key's value; with three, stretches at the ends and
+    around the offsets of 2^31 and 2^32 elements against fp64."""
+    Lq, H, D = (1 << 28) + 5, 8, 8
+    g = torch.Generator(device="cuda").manual_seed(Lk)
+    q = torch.randn(1, Lq, 1, D, generator=g, device="cuda", dtype=torch.bfloat16).expand(1, Lq, H, D)
+    k, v = (torch.randn(1, Lk, H, D, generator=g, device="cuda", dtype=torch.bfloat16) for _ in range(2))
+    out = torch.full((1, Lq + 1, H, D), 3.0, dtype=torch.bfloat16, device="cuda")
+    try:
+        o = tern.attention(q, k, v, out=out[:, :Lq])
+        assert (out[:, Lq] == 3).all() and tern.device_status() == 0
+        if Lk == 1:
+            for at in range(0, Lq, 1 << 24):
+                assert (o[:, at:at + (1 << 24)] == v).all()
+            return
+        kernel = tern.attention_plan(q, k, v)[0]
+        for at in (0, (1 << 25) - 500, (1 << 26) - 500, (1 << 27) + 77, Lq - 1000):
+            close(o[:, at:at + 1000], q[:, at:at + 1000], k, v, kernel)
+    finally:
+        del out, q
+        o = None
+        torch.cuda.empty_cache()
