@@ -946,8 +946,44 @@ bool elements_distinct(const Heads& t) {
   return true;
 }
 
-// Whether two head tensors share a byte: by their spans, or exactly (as
-// regions of rows) where both are column slices of rows equally far apart.
+// Whether two head tensors that share their strides share an element: whether
+// their starts differ by a sum of t_i strides, each |t_i| within the sizes, and less
+// than D elements.  With the larger strides first, what the remaining terms can
+// reach leaves a few values of t_i where strides nest; where they leave many
+// (inputs whose elements lie over one another) the answer is yes.
+struct Step {
+  int64_t stride, lo, hi;  // t_i in [lo, hi]
+};
+bool steps_meet(const Step* d, int n, int64_t rest, int64_t width) {
+  if (n == 0) return rest < width && rest > -width;
+  int64_t reach = width - 1;
+  for (int i = 1; i < n; ++i) reach += std::max(-d[i].lo, d[i].hi) * d[i].stride;
+  auto floor_div = [](int64_t x, int64_t y) { return x / y - (x % y < 0); };
+  const int64_t from = std::max(d->lo, -floor_div(reach - rest, d->stride)), to = std::min(d->hi, floor_div(rest + reach, d->stride));
+  if (to - from > 3) return true;
+  for (int64_t t = from; t <= to; ++t)
+    if (steps_meet(d + 1, n - 1, rest - t * d->stride, width)) return true;
+  return false;
+}
+bool elements_meet(const Heads& a, const Heads& b) {
+  const int64_t na[3] = {a.B, a.L, a.H}, nb[3] = {b.B, b.L, b.H}, sa[3] = {a.b, a.l, a.h}, sb[3] = {b.b, b.l, b.h};
+  Step d[3];
+  int n = 0;
+  for (int i = 0; i < 3; ++i) {
+    if (na[i] <= 1 && nb[i] <= 1) continue;
+    if (na[i] > 1 && nb[i] > 1 && sa[i] != sb[i]) return true;  // other strides
+    const int64_t s = na[i] > 1 ? sa[i] : sb[i];
+    if (s > 0) d[n++] = Step{s, 1 - nb[i], na[i] - 1};
+  }
+  std::sort(d, d + n, [](const Step& x, const Step& y) { return x.stride > y.stride; });
+  // 16-byte alignment: the difference is whole elements
+  const int64_t apart = int64_t(reinterpret_cast<uintptr_t>(b.p) - reinterpret_cast<uintptr_t>(a.p)) / 2;
+  return steps_meet(d, n, apart, a.D);
+}
+
+// Whether two head tensors share a byte: by their spans; as regions of rows
+// where both are column slices of rows equally far apart; element by element
+// where they share all strides.
 bool heads_overlap(const Heads& a, const Heads& b) {
   if (a.empty() || b.empty()) return false;
   if (!overlaps(a.p, size_t(a.span()) * 2, b.p, size_t(b.span()) * 2)) return false;
@@ -958,8 +994,10 @@ bool heads_overlap(const Heads& a, const Heads& b) {
     return true;
   };
   int64_t na, wa, nb, wb;
-  if (a.l <= 0 || a.l != b.l || !rows(a, &na, &wa) || !rows(b, &nb, &wb)) return true;
-  return regions_overlap(a.p, na, size_t(wa) * 2, size_t(a.l) * 2, b.p, nb, size_t(wb) * 2, size_t(b.l) * 2);
+  if (a.l > 0 && a.l == b.l && rows(a, &na, &wa) && rows(b, &nb, &wb) &&
+      !regions_overlap(a.p, na, size_t(wa) * 2, size_t(a.l) * 2, b.p, nb, size_t(wb) * 2, size_t(b.l) * 2))
+    return false;
+  return elements_meet(a, b);
 }
 
 bool overlaps_flat(const Heads& t, const void* p, size_t bytes) {

@@ -409,8 +409,9 @@ typedef struct {
  * elements of y distinct: y's strides nest, in either order of tokens and
  * heads, inside its batch stride.  B, L >= 0 and heads >= 0; none is a no-op.
  * No y overlaps another tensor's x or y, or the table: regions are compared
- * by their spans, unless they share their strides and lie in different
- * channels or heads of one parent's rows.
+ * by their spans, unless they are column slices of rows equally far apart, or
+ * share all strides (channels, heads or entries of one parent): those may
+ * lie between one another.
  */
 TERN_API tern_status tern_rope(const tern_rope_tensor* tensors, int count, int64_t B, int64_t L, int64_t head_dim,
                                const float* cs, int64_t cs_rows, int64_t P, int layout, tern_stream_t stream);

@@ -304,3 +304,41 @@ def test_attention_takes_as_many_query_rows_as_documented(L):
     assert _attn(L, **far, Lq=(1 << 30) - 1, Lk=0, kv_len=1) == MISALIGNED  # refused for that alone
     far.update(H=32, Hkv=32, o_l=256)
     assert _attn(L, **far, Lq=1 << 29, Lk=3) == SHAPE
+
+
+def _heads(t):
+    """(address, strides) of a [B, L, H, D] view of a bf16 tensor on the host, as if it lay at F."""
+    return F + 2 * t.storage_offset(), t.stride()[:3]
+
+
+def test_slices_of_one_parent_may_lie_between_one_another(L):
+    """Every pair of slices of a small parent, in several layouts, against the sets of their elements."""
+    if torch.cuda.is_available():
+        pytest.skip("accepted calls would launch")
+    B, n, H, D = 2, 3, 2, 16
+    cs = dict(B=B, n=n, D=D, P=8, cs=F - 0x10000)
+    parents = {"between heads": bf(B, n, H, 3, D), "heads first": bf(B, 3, H, n, D).permute(0, 3, 2, 1, 4),
+               "entries first": bf(3, B, n, H, D).permute(1, 2, 3, 0, 4), "tokens last": bf(3, H, B, n, D).permute(2, 3, 1, 0, 4)}
+    count = 0
+    for z in parents.values():
+        at = torch.arange(z.numel()).view(-1).as_strided(z.shape, z.stride())
+        views = [z[:, :, :, i] for i in range(3)]
+        ids = [at[:, :, :, i] for i in range(3)]
+        for i in range(3):
+            for off in (0, 8, 16, 24, 40, z.stride(2), z.stride(1) - 8, z.stride(0) + 8):
+                for j in range(3):
+                    (a, sa), (b, sb) = _heads(views[i]), _heads(views[j])
+                    b += 2 * off
+                    meet = bool(np.intersect1d(ids[i].numpy(), ids[j].numpy() + off).size)
+                    got = _rope(L, [(a, a, H, *sa, *sa), (b, b, H, *sb, *sb)], **cs)
+                    assert (got == INVALID) == meet and got in (INVALID, -4, -6), (i, j, off, got, meet)
+                    count += not meet
+    assert count > 50
+    # attention's output between its inputs, and over one of them
+    z = bf(B, n, H, 4, D)
+    kw = {}
+    for i, name in enumerate("qkvo"):
+        a, s = _heads(z[:, :, :, i])
+        kw.update({name: a, **{f"{name}_{x}": v for x, v in zip("blh", s)}})
+    kw.update(B=B, Lq=n, Lk=n, H=H, Hkv=H, D=D)
+    assert _attn(L, **kw) in (-4, -6) and _attn(L, **{**kw, "o": kw["o"] - 16}) == INVALID

@@ -316,3 +316,15 @@ def test_more_than_2_to_the_31_query_rows(Lk):
         del out, q
         o = None
         torch.cuda.empty_cache()
+
+
+@pytest.mark.parametrize("B,L,H,D", [(2, 9, 4, 64), (1, 700, 24, 128)])
+def test_output_between_its_inputs(B, L, H, D):
+    """o, q, k and v side by side in every head of one tensor."""
+    z = rand((B, L, H, 4, D), 1, 1.4).cuda()
+    q, k, v, o = (z[:, :, :, i] for i in range(4))
+    old = z.clone()
+    kernel = tern.attention_plan(q, k, v)[0]
+    assert kernel == (TILES if L == 700 else ROWS)
+    close(tern.attention(q, k, v, out=o), q, k, v, kernel)
+    assert torch.equal(z[:, :, :, :3], old[:, :, :, :3])

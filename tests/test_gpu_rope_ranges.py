@@ -30,3 +30,21 @@ def test_rotation_of_as_many_rows_as_there_may_be(rows):
         del y
         words = None
         torch.cuda.empty_cache()
+
+
+@pytest.mark.parametrize("halves", [False, True])
+@pytest.mark.parametrize("layout", ["between heads", "heads first", "entries first"])
+def test_rotation_in_place_of_slices_that_lie_between_one_another(layout, halves):
+    """q and k of a projection whose heads hold q, k and v side by side, or of
+    a tensor [B, 3, H, L, D] or [3, B, L, H, D]: turned in place, v as it was."""
+    B, L, H, D = 2, 37, 5, 64
+    g = torch.Generator().manual_seed(2)
+    shape, order = {"between heads": ((B, L, H, 3, D), (0, 1, 2, 3, 4)), "heads first": ((B, 3, H, L, D), (0, 3, 2, 1, 4)),
+                    "entries first": ((3, B, L, H, D), (1, 2, 3, 0, 4))}[layout]
+    z = torch.randn(shape, generator=g).to(torch.bfloat16).cuda().permute(order)
+    q, k, v = (z[:, :, :, i] for i in range(3))
+    cs = tern.rope_table(torch.arange(L).float()[:, None].cuda(), (48,))
+    want = tern.rope([q.clone(), k.clone()], cs, halves=halves)
+    keep = v.clone()
+    tern.rope([q, k], cs, halves=halves, outs=[q, k])
+    assert torch.equal(q, want[0]) and torch.equal(k, want[1]) and torch.equal(v, keep)
