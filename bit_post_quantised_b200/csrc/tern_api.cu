@@ -914,6 +914,7 @@ tern_status tern_linear_e4m3(const void* xq, const float* a, int64_t M, int64_t 
 namespace {
 
 constexpr int64_t kMaxStride = int64_t(1) << 38;
+constexpr int64_t kMaxSpan = int64_t(1) << 56;  // elements: as far as addresses go; sums of spans stay in 64 bits
 
 // A [B, L, heads, D] bf16 tensor: strides in elements, adjacent channels.
 struct Heads {
@@ -928,7 +929,7 @@ struct Heads {
 bool strides_ok(const Heads& t, bool read) {
   const int64_t n[3] = {t.B, t.L, t.H}, s[3] = {t.b, t.l, t.h};
   for (int i = 0; i < 3; ++i)
-    if (n[i] > 1 && (s[i] % 8 != 0 || s[i] < (read ? 0 : 8) || s[i] > kMaxStride)) return false;
+    if (n[i] > 1 && (s[i] % 8 != 0 || s[i] < (read ? 0 : 8) || s[i] > kMaxStride || s[i] > kMaxSpan / (n[i] - 1))) return false;
   return true;
 }
 
@@ -1305,7 +1306,7 @@ tern_status tern_gated_residual_norm(const tern_gated_residual_norm_args* args, 
   if (!aligned(t.x, 16) || !aligned(t.o, 16) || !aligned(t.x_out, 16) || !aligned(t.h, 16) || !aligned(t.gate, 16) ||
       !aligned(t.scale, 16) || !aligned(t.shift, 16) || !aligned(t.post_weight, 16) || !aligned(t.pre_weight, 16))
     return fail(TERN_ERR_MISALIGNED, "every tensor needs 16-byte alignment");
-  auto row_stride = [&](int64_t ld) { return ld >= t.K && ld % 8 == 0 && ld <= kMaxStride; };
+  auto row_stride = [&](int64_t ld) { return ld >= t.K && ld % 8 == 0 && ld <= std::min(kMaxStride, kMaxSpan / t.M); };
   if (!row_stride(t.ld_x) || !row_stride(t.ld_o) || !row_stride(t.ld_x_out) || (t.h && !row_stride(t.ld_h)))
     return fail(TERN_ERR_INVALID_ARG, "row strides need >= K=%lld and multiples of 8", (long long)t.K);
   const bool mod = t.gate || t.scale;

@@ -342,3 +342,15 @@ def test_slices_of_one_parent_may_lie_between_one_another(L):
         kw.update({name: a, **{f"{name}_{x}": v for x, v in zip("blh", s)}})
     kw.update(B=B, Lq=n, Lk=n, H=H, Hkv=H, D=D)
     assert _attn(L, **kw) in (-4, -6) and _attn(L, **{**kw, "o": kw["o"] - 16}) == INVALID
+
+
+def test_strides_that_reach_past_all_addresses_are_refused(L):
+    """(B - 1) * stride of 2^68 elements: no overlap check in 64 bits holds there."""
+    far = 1 << 38
+    assert _rope(L, [(F, F, 1, far, 16, 16, far, 16, 16)], B=1 << 30, n=1, D=16, P=8) == INVALID
+    assert _rope(L, [(F, F, 1, 16, far, 16, 16, far, 16)], B=1, n=1 << 30, D=16, P=8) == INVALID
+    assert _attn(L, B=1, Lq=1 << 29, H=1, Hkv=1, q_l=far, o=F + 0x5000000) == INVALID
+    assert _attn(L, B=1, Lk=1 << 29, H=1, Hkv=1, k_l=far) == INVALID and _attn(L, B=1, Lk=1 << 29, H=1, Hkv=1, v_l=far) == INVALID
+    for n in ("ld_x", "ld_o", "ld_x_out", "ld_h"):
+        assert _norm(L, M=(1 << 31) - 1, x=F, x_out=F, o=F + (1 << 40), h=F + (1 << 40), tokens_per_row=1 << 31,
+                     **{"ld_x": 256, "ld_o": 256, "ld_x_out": 256, "ld_h": 256, n: far}) == INVALID
