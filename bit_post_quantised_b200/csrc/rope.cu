@@ -59,12 +59,12 @@ __device__ __forceinline__ float2 cos_sin(double x, double w) {
 
 __global__ void __launch_bounds__(kTableThreads)
     rope_table_kernel(const float* __restrict__ ids, int L, const __grid_constant__ RopeFreqs f, float2* cs) {
-  extern __shared__ float2 tile[];  // [kTableRows][pairs + 1]: a column of lanes meets every bank
+  extern __shared__ float2 tile[];  // [kTableRows][pairs | 1]: a column of lanes meets every bank
   pdl_wait();
   pdl_trigger();
-  const int P = f.pairs, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int P = f.pairs, pitch = P | 1, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int m0 = int(blockIdx.x) * kTableRows, rows = min(kTableRows, L - m0);
-  float2* const row = tile + lane * (P + 1);
+  float2* const row = tile + lane * pitch;
   int end = 0;
 #pragma unroll 1
   for (int a = 0; a < f.n_axes; ++a) {
@@ -76,7 +76,7 @@ __global__ void __launch_bounds__(kTableThreads)
   __syncthreads();
   float2* out = cs + (long long)m0 * P;
   for (int r = warp; r < rows; r += kTableThreads / 32)
-    for (int j = lane; j < P; j += 32) out[r * P + j] = tile[r * (P + 1) + j];
+    for (int j = lane; j < P; j += 32) out[r * P + j] = tile[r * pitch + j];
 }
 
 // ---------------------------------------------------------------- rotation
@@ -172,7 +172,7 @@ __global__ void __launch_bounds__(256) rope_kernel(const __grid_constant__ RopeA
 
 cudaError_t launch_rope_table(const float* ids, int L, const RopeFreqs& f, float* cs, cudaStream_t stream) {
   const unsigned grid = (unsigned(L) + kTableRows - 1) / kTableRows;
-  return launch_pdl(rope_table_kernel, dim3(grid), dim3(kTableThreads), kTableRows * (f.pairs + 1) * sizeof(float2), stream,
+  return launch_pdl(rope_table_kernel, dim3(grid), dim3(kTableThreads), kTableRows * (f.pairs | 1) * sizeof(float2), stream,
                     1, ids, L, f, reinterpret_cast<float2*>(cs));
 }
 

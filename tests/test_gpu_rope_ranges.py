@@ -1,11 +1,12 @@
 """tern_rope and tern_rope_table at the ends of their documented ranges, on the GPU."""
 from __future__ import annotations
 
+import numpy as np
+import pytest
 import torch
 
-import pytest
-
 from bit_post_quantised_b200 import tern
+from oracle import block_ops as ref
 
 pytestmark = pytest.mark.gpu
 
@@ -48,3 +49,15 @@ def test_rotation_in_place_of_slices_that_lie_between_one_another(layout, halves
     keep = v.clone()
     tern.rope([q, k], cs, halves=halves, outs=[q, k])
     assert torch.equal(q, want[0]) and torch.equal(k, want[1]) and torch.equal(v, keep)
+
+
+@pytest.mark.parametrize("L,axes", [(70, (42, 42, 42)), (33, (62,)), (1, (6,)), (97, (2, 200, 48, 4))])
+def test_tables_of_odd_pair_counts(L, axes):
+    """One rounding to fp32 (2^-24 relative), the 64-bit angle's error (2^-50 of
+    it) and the polynomials' truncation (below 1e-11), as for even counts."""
+    ids = torch.randint(-50, 5000, (L, len(axes)), generator=torch.Generator().manual_seed(L)).float()
+    ang, want = ref.rope_angles(ids.numpy(), axes, 1e4), ref.rope_table(ids.numpy(), axes, 1e4)
+    out = torch.full((L + 1, sum(axes) // 2, 2), 7.0, device="cuda")
+    got = tern.rope_table(ids.cuda(), axes, out=out[:L]).cpu().double().numpy()
+    assert np.all(np.abs(got - want) <= ref.F32 * np.abs(want) + (np.abs(ang) * 2.0 ** -50)[..., None] + 1e-11)
+    assert (out[L] == 7).all()
