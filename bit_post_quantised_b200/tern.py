@@ -548,7 +548,8 @@ def attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, scale: Optional
     channels; H / Hkv query heads share a key-value head; scale defaults to
     1 / sqrt(D).  kv_len int32 [B] and key_mask bool or uint8 [B, Lk] (without
     B: [1] and [Lk]) say which keys count; a batch entry without one gives
-    zeros.  Returns [B, Lq, H, D] (contiguous, or `out`)."""
+    zeros.  Where `attention_plan` says tiles, probabilities meet v as bf16;
+    all else is fp32.  Returns [B, Lq, H, D] (contiguous, or `out`)."""
     sq, sk, sv = _bf16("q", q, (3, 4)), _bf16("k", k, (3, 4)), _bf16("v", v, (3, 4))
     nd = len(sq)
     if len(sk) != nd or len(sv) != nd:

@@ -362,8 +362,8 @@ TERN_API tern_status tern_linear_e4m3(const void* xq, const float* a, int64_t M,
  * Operators of a transformer block between its linears.  The pages describe
  * nothing there (Section 3.1 names the linears only): these are interface
  * choices of this library.  bf16 in and out, fp32 (or better) inside, one
- * rounding per output.  No workspace, one launch each; strides are in
- * elements.
+ * rounding per output; the one exception is tern_attention's probabilities (see
+ * there).  No workspace, one launch each; strides are in elements.
  */
 
 /*
@@ -424,12 +424,20 @@ TERN_API tern_status tern_rope(const tern_rope_tensor* tensors, int count, int64
  * values hold (infinities and NaN too) does not reach the output; scores that
  * are NaN, or infinite (of either sign, in fp32 and with the scale) at their
  * row's maximum, give NaN rows.
+ * Scores, maxima, sums and the output's accumulator are fp32.  A probability
+ * enters its product with v as one bf16 where the call takes tiles (off by
+ * 2^-8 of itself at most; the sum that divides is of the unrounded ones; the
+ * output's error, in rms, is then 1.25 to 1.4 times that of its own rounding, as
+ * measured).  Where the call takes rows it enters as two bf16, value and
+ * remainder (2^-16).  tern_attention_plan says which: it depends on the sizes, the
+ * strides and the GPU, so the same rows may differ in their last bits between
+ * calls of other sizes.
  *   q, o      [B, Lq, H, D];  k, v  [B, Lk, Hkv, D]; channels are adjacent.
  *   kv_len    [B] int32 device memory or NULL (all Lk); clamped to [0, Lk].
  *   key_mask  [B, Lk] bytes device memory, rows mask_ld apart, or NULL.
  * H % Hkv == 0, D % 8 == 0, 8 <= D <= 128, Lq, Lk < 2^30, B * H < 2^20 and
  * B * H * Lq < 2^34 (TERN_ERR_UNSUPPORTED_SHAPE); pointers 16-byte aligned, strides multiples
- * of 8 below 2^38, 0 allowed in q, k and v (a broadcast); the elements of o
+ * of 8 up to 2^38, 0 allowed in q, k and v (a broadcast); the elements of o
  * are distinct (strides as tern_rope's y) and o overlaps no input.  scale > 0
  * and below 2^127.  B, Lq or H == 0 is a no-op; Lk == 0 writes zeros (k and v may
  * be NULL).
