@@ -26,7 +26,7 @@
 // CTAs shares the keys of one: each runs its own key tiles, leaves O and (m,
 // sum) in its ring once that is done with, and joins a part of the rows through
 // distributed shared memory (2 x 300 x 4000 x 6 heads of 64: 50 -> 21 us, 512 x
-// 16,384 x 8 of 128: 205 -> 64).  No workspace, and the same order every time.
+// 16,384 x 8 of 128: 205 -> 65).  No workspace, and the same order every time.
 //
 // The reference m only follows the running maximum when that has grown by
 // more than 8 in log2 units: until then probabilities are at most 2^8, which
@@ -42,7 +42,7 @@
 // 300, exponentials 1450 of at least 1024, barriers) and then the product and
 // the next scores (1024 and their latencies): a period of some 3300 cycles,
 // with the two query tiles half a period apart; 4608 x 4608 x 24 heads take
-// 198 us, 0.77 of the measured cuBLAS rate.  Tried and slower: part of the
+// 200 us, 0.77 of the measured cuBLAS rate.  Tried and slower: part of the
 // exponentials as polynomials on the FMA pipe (the softmax is bound by its
 // dependent issue, not by the exponentials' pipe alone: +3 to +9%), 64-key
 // steps with two score buffers a query tile (scores of 64 keys read Q from

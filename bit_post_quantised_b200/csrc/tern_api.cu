@@ -1041,11 +1041,14 @@ AttnChoice choose_attention(const tern_attention_args& t, int sms) {
   // wave of its CTAs (two an SM) the 16-key blocks that a warp takes one after
   // the other; tiles: a start, and for every round of units over the SMs its
   // key tiles, however few of a tile's rows there are.  Measured (us, rows |
-  // tiles): 24 heads of 128, 512 keys: 32 queries 8.4 | 9.1, 64 queries 11.4 |
-  // 9.1; 4096 keys: 32 queries 23 | 50, 96 queries 39 | 50; 64 x 1 query of 8 heads, 4096
-  // keys 154 | 193; 4 heads of 64, 256 x 256 5.3 | 6.9; 24 heads of 64, 256 x 77
-  // 9.8 | 5.7.  (A tensor map has no dimension of stride 0: tokens that are one
-  // broadcast row take rows.)
+  // tiles, the keys shared as below): 24 heads of 128, 512 keys: 32 queries 8.5 |
+  // 9.3, 64 queries 11.7 | 9.4; 4096 keys: 32 queries 21.3 | 25.5, 96 queries 38 |
+  // 25.8; 64 x 1 query of 8 heads, 4096 keys 155 | 199; 4 heads of 64, 256 x 256
+  // 5.5 | 7.1; 24 heads of 64, 256 x 77 9.9 | 5.7.  Over 60 mixed shapes the
+  // choice is within 2 % of the best for 51 and within 10 % for 56; it is furthest
+  // off where many short units take tiles (3 x 4 x 22, 24 heads of 128, masked 7.0
+  // against 4.7), since nothing stands for a unit's own start.  (A tensor map has
+  // no dimension of stride 0: tokens that are one broadcast row take rows.)
   const bool flat = (t.Lq > 1 && t.q_l == 0) || (t.Lk > 1 && (t.k_l == 0 || t.v_l == 0));
   const int64_t pairs = (t.Lq + 255) / 256, tile_units = pairs * t.B * t.H;
   const int64_t row_units = (t.Lq * (t.H / t.Hkv) + 15) / 16 * t.Hkv * t.B;
@@ -1056,11 +1059,12 @@ AttnChoice choose_attention(const tern_attention_args& t, int sms) {
   const bool wide = t.D > 64;
   const double rows_us = 2.5 + (splits > 1 ? 1. : 0.) + double(waves) * (wide ? 2.5 + 1.05 * blocks : 1.2 + 0.65 * blocks);
   // Where units leave SMs idle, a cluster of CTAs shares the keys of each, as
-  // far as all clusters are resident at once (of 8 CTAs with an SM each: 64
-  // CTAs in one wave, 128 in two).  The join takes 2.5 us and 1.6 a CTA.
-  // Measured (us, 1 | 2 | 4 | 8 CTAs): 256 x 4608 x 8 heads of 128 61 | 39 | 27 |
-  // 25, 512 x 16,384 x 8 206 | 113 | 64 | -, 1024 x 1024 x 8 18 | 16.6 | 17.5 |
-  // -, 256 x 512 x 8 11 | 13 | 14 | 17, 2 x 300 x 4000 x 6 of 64 50 | 30 | 21 | -.
+  // far as all clusters are resident at once: on a B200's 148 SMs 64 CTAs in
+  // clusters of 8, 128 in smaller ones (a limit for speed alone: clusters do not wait
+  // for one another).  The join takes 2.5 us and 1.6 a CTA.  Measured (us, 1 | 2 |
+  // 4 | 8 CTAs): 256 x 4608 x 8 heads of 128 62 | 39 | 27 | 26, 512 x 16,384 x 8
+  // 210 | 115 | 67 | -, 1024 x 1024 x 8 18.3 | 17.0 | 18.5 | -, 256 x 512 x 8 11.5
+  // | 13 | 14 | 18, 2 x 300 x 4000 x 6 of 64 51 | 31 | 21 | -.
   const double tile_us = wide ? (t.Lq > 128 ? 1.6 : 1.47) : t.Lq > 128 ? 1.4 : 0.98;
   auto tiles_time = [&](int n) {
     return (wide ? 3.3 : 4.9) + (n > 1 ? 2.5 + 1.6 * n : 0.) + tile_us * double(rounds) * double((tiles + n - 1) / n);

@@ -28,7 +28,8 @@ states' keys and values come from a ternary projection of their own, the
 queries are the block's normalised ones before rotation, and what comes back
 is normalised and enters the stream through a tanh gate together with the
 norm before the MLP.  Rotation then follows as an operation of its own
-instead of in the projection's epilogue.  All of it runs in the library
+instead of in the projection's epilogue, so q and k of those blocks are
+rounded to bf16 after their norm and once more after rotation.  All of it runs in the library
 (``tern.rope_table``, ``tern.attention``, ``tern.rope``,
 ``tern.gated_residual_norm``); without context nothing changes.
 
