@@ -241,15 +241,16 @@ def test_rows_whose_scores_are_all_minus_infinity(size, kernel, ctas, raw):
         assert torch.equal(got[0, rest], want[0, rest]) and torch.equal(got[1:], want[1:])
 
 
-@pytest.mark.parametrize("size,kernel,ctas", CASES)
+QUARTERS = [c for c in CASES if c[0][2] >= 8]  # keys enough for a quarter of them
+
+
+@pytest.mark.parametrize("size,kernel,ctas", QUARTERS)
 @pytest.mark.parametrize("raw", [True, False])
 @pytest.mark.parametrize("where", ["first", "last"])
 def test_keys_at_minus_infinity_before_and_behind_finite_ones(size, kernel, ctas, raw, where):
     """Three quarters of the keys score -inf with every query, raw or by the
     scale; the rest decide, as if those keys were not there."""
     B, Lq, Lk, H, Hkv, D = size
-    if Lk < 8:
-        pytest.skip("no quarter")
     q, k, v = inputs(*size)
     goes(q, k, v, kernel, ctas)
     gone = torch.arange(Lk, device="cuda") < Lk - Lk // 4
@@ -270,13 +271,11 @@ def test_keys_at_minus_infinity_before_and_behind_finite_ones(size, kernel, ctas
     assert np.all(np.abs(got - want) <= ref.BF16 * (np.abs(want) + e) + e)
 
 
-@pytest.mark.parametrize("size,kernel,ctas", CASES)
+@pytest.mark.parametrize("size,kernel,ctas", QUARTERS)
 def test_minus_infinity_under_a_mask(size, kernel, ctas):
     """The valid keys score -inf, the masked ones would not: NaN rows; an entry
     without a valid key is zeros beside them."""
     B, Lq, Lk, H, Hkv, D = size
-    if Lk < 8:
-        pytest.skip("no quarter")
     q, k, v = inputs(2, *size[1:])
     m = torch.zeros(2, Lk, dtype=torch.bool, device="cuda")
     m[0, Lk // 2:Lk // 2 + Lk // 4] = True
